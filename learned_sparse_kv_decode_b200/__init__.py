@@ -2,7 +2,8 @@
 
 The chunk-scoring, top-k, gather and sparse flash-decode kernels live in
 ``liblsa_b200.so`` (sources in ``csrc/``, C ABI in ``include/lsa.h``);
-``abi`` is the thin ctypes binding with the same entry-point names. The library
+``abi`` is the thin ctypes binding with the same entry-point names; the 8-bit K/V cache
+(``include/lsa_kv8.h``) has its binding in ``kv8``. The library
 must be built (``learned_sparse_kv_decode_b200.build.build()``): there is no
 fallback when it is missing.
 
@@ -24,4 +25,8 @@ from .abi import (  # noqa: E402,F401
     lsa_sparse_decode_attn_lookahead, lsa_decode_step_lookahead, lsa_lookahead_partition,
     LSA_OK, LSA_ERR_INVALID_ARG, LSA_ERR_WORKSPACE, LSA_ERR_CUDA, LSA_ERR_NONFINITE,
     LSA_ERR_TIMEOUT, LSA_ERR_UNSUPPORTED, LSA_ERR_BAD_ID, LSA_F32, LSA_BF16,
+)
+from .kv8 import (  # noqa: E402,F401
+    Kv8Cache, QkPrep, alloc_kv8_cache, kv8_header_symbols, lsa_decode_step_kv8, lsa_kv8_append,
+    lsa_kv8_decode_attn, lsa_kv8_gather, lsa_kv8_workspace_size, lsa_qk_norm_rope,
 )

@@ -289,8 +289,14 @@ def lsa_read_stream(buf, stream=None) -> None:
     _check(lib.lsa_read_stream(_p(buf), _nbytes(buf), _stream(stream)), "lsa_read_stream")
 
 
-def alloc_workspace(dims: Dims, device=None, stream=None):
-    """Allocate (with torch) and initialise a workspace for ``dims``."""
-    ws = torch.empty(lsa_workspace_size(dims), dtype=torch.uint8, device=device or "cuda")
+def alloc_workspace(dims: Dims, device=None, stream=None, kv8=None):
+    """Allocate (with torch) and initialise a workspace for ``dims``; with ``kv8`` (a Kv8Cache) one that
+    also serves the calls on that cache."""
+    if kv8 is None:
+        size = lsa_workspace_size(dims)
+    else:
+        from .kv8 import lsa_kv8_workspace_size
+        size = lsa_kv8_workspace_size(dims, kv8)
+    ws = torch.empty(size, dtype=torch.uint8, device=device or "cuda")
     lsa_workspace_init(ws, stream)
     return ws

@@ -6,7 +6,7 @@
 #include <cstring>
 #include <mutex>
 
-#include "lsa_device.cuh"
+#include "lsa_host.cuh"
 
 namespace lsa {
 cudaError_t launch_score(const lsa_dims& d, const SeqTable& tab, int max_n, const void* q_emb,
@@ -31,6 +31,7 @@ cudaError_t score_init_attrs();
 cudaError_t topk_init_attrs();
 cudaError_t refresh_init_attrs();
 cudaError_t fp8_init_attrs();
+cudaError_t kv8_init_attrs(int num_sms, int* ctas);
 struct ShardOffsets {
     int32_t global0[kMaxB];
 };
@@ -72,15 +73,12 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-    bool ready;
-    int sms;
-    int attn_ctas[2];  // per kv dtype (LSA_F32, LSA_BF16)
-    int la_ctas;       // CTAs of the lookahead-window attention
-};
-
 std::mutex g_dev_mu;
 DeviceInfo g_dev[kMaxDevices];
+
+}  // namespace
+
+namespace lsa {
 
 // SM count and attention CTAs per device, computed once per device.
 lsa_status device_info(DeviceInfo* out) {
@@ -101,22 +99,12 @@ lsa_status device_info(DeviceInfo* out) {
         int la_occ = 0;
         if (la_init_attrs(&la_occ) != cudaSuccess || la_occ < 1) return LSA_ERR_CUDA;
         di.la_ctas = la_occ * sms;
+        if (kv8_init_attrs(sms, &di.kv8_ctas) != cudaSuccess) return LSA_ERR_CUDA;
         di.ready = true;
     }
     *out = di;
     return LSA_OK;
 }
-
-bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
-bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-struct Prepared {
-    SeqTable tab;
-    int max_n;
-    int64_t total_chunks;
-    int64_t total_kept;
-};
 
 // Validate the shape and build the per-sequence table.
 lsa_status prepare(const lsa_dims* d, Prepared* p) {
@@ -166,12 +154,8 @@ lsa_status prepare(const lsa_dims* d, Prepared* p) {
     return LSA_OK;
 }
 
-struct WsLayout {
-    size_t scores, part_o, part_ml, ids, copy_src, copy_dst, copy_count, la_o, la_ml, small, total;
-};
-
 // The lookahead-window attention runs for bf16 K/V and windows of up to 64 queries.
-bool la_shape(const lsa_dims* d) { return d->kv_dtype == LSA_BF16 && d->Q <= la_max_queries(); }
+static bool la_shape(const lsa_dims* d) { return d->kv_dtype == LSA_BF16 && d->Q <= la_max_queries(); }
 
 // Workspace: header (sticky error word; arrival counters of the one-launch step) | scores |
 // split partials | refresh buffers | lookahead partials | one-launch step partials.
@@ -196,6 +180,10 @@ WsLayout ws_layout(const lsa_dims* d, const Prepared& p, const DeviceInfo& di) {
     return w;
 }
 
+}  // namespace lsa
+
+namespace {
+
 // Validation shared by every call that takes a workspace.
 lsa_status prepare_ws(const lsa_dims* d, void* ws, size_t ws_bytes, Prepared* p, DeviceInfo* di,
                       WsLayout* w) {
@@ -208,9 +196,6 @@ lsa_status prepare_ws(const lsa_dims* d, void* ws, size_t ws_bytes, Prepared* p,
     if (ws_bytes < w->total) return LSA_ERR_WORKSPACE;
     return LSA_OK;
 }
-
-inline uint8_t* at(void* ws, size_t off) { return static_cast<uint8_t*>(ws) + off; }
-inline lsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? LSA_OK : LSA_ERR_CUDA; }
 
 }  // namespace
 
