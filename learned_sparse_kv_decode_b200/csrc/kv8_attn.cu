@@ -35,6 +35,7 @@ namespace lsa {
 constexpr int kKv8Warps = 4;
 constexpr int kKv8Threads = kKv8Warps * 32;
 constexpr int kKv8CtasPerSm = 3;
+constexpr int kKv8Stages = 4;      // tiles of a warp's ring
 constexpr int kKv8Tile = 16;       // tokens per tile
 constexpr int kKv8MaxRows = 8;     // query heads per run
 constexpr float kKv8PShift = 14.f; // weights are at most 2^14
@@ -83,68 +84,75 @@ __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
     return r;
 }
 
-// 16 bytes that are not kept in L1. Not a non-coherent load: in the fused step this kernel is resident
-// while the kernel that writes the newest row still runs.
-__device__ __forceinline__ uint4 kv8_ld16(const void* p) {
+// ---------------------------------------------------------------- a warp's ring of tiles
+// One slot: 16 rows of K, 16 rows of V (128 bytes each), then the tile's scales and token counts. A
+// row's 16-byte units are XOR-swizzled by the row, so that both fragment reads are free of conflicts.
+constexpr int kKv8SlotK = 0;
+constexpr int kKv8SlotV = kKv8Tile * kDh;
+constexpr int kKv8SlotMeta = 2 * kKv8Tile * kDh;  // ks[2], vs[2] (float), n[2] (int)
+constexpr int kKv8SlotBytes = kKv8SlotMeta + 32;
+constexpr int kKv8WarpBytes = kKv8Stages * kKv8SlotBytes;
+constexpr int kKv8JoinBytes = kKv8Warps * kKv8MaxRows * (kDh + 2) * 4;
+constexpr int kKv8Smem = kKv8Warps * kKv8WarpBytes > kKv8JoinBytes ? kKv8Warps * kKv8WarpBytes : kKv8JoinBytes;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 kv8_lds16(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
 
-// What a warp knows of one tile: its two octets (8 tokens each) of K and V, their scales, and how many
-// tokens of each octet take part.
-struct Kv8Octets {
-    uint32_t k[2][8];
-    uint4 v[4];
-    float ks[2], vs[2];
-    int n[2];
+// The run that a warp streams.
+struct Kv8Run {
+    int64_t chunk0;      // first chunk of the sequence
+    int64_t len;         // tokens of the sequence that exist
+    const int32_t* ids;  // nullable
+    int n_b, kept, h;
 };
 
-// One tile's loads. `t0` is its first token within the run; the ids of its chunks are id[0], id[1].
-__device__ __forceinline__ void kv8_load(Kv8Octets& o, const Kv8AttnParams& p, int64_t chunk0, int n_b, int h,
-                                         int kept, int64_t len, int t0, const int* id, int g, int t,
-                                         uint32_t* err) {
-    const int C = 1 << p.g.c_log2;
+// Start the copies of one tile into `slot`: first token t0 within the run, the ids of its two octets'
+// chunks. The counts n are what the consumer goes by: an octet without tokens is not copied.
+__device__ __forceinline__ void kv8_issue(uint32_t slot, const Kv8AttnParams& p, const Kv8Run& r, int t0, int id0,
+                                          int id1, int lane, uint32_t* err) {
+    const int cm = (1 << p.g.c_log2) - 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int tk = t0 + 8 * i;
-        const int j = tk >> p.g.c_log2, w = tk & (C - 1);
+        const int tk = t0 + 8 * i, id = i ? id1 : id0;
+        const int j = tk >> p.g.c_log2, w = tk & cm;
         int n = 0;
-        if (j < kept) {
-            if (id[i] >= 0 && id[i] < n_b) {
-                const int64_t left = len - (((int64_t)id[i] << p.g.c_log2) + w);
+        if (j < r.kept) {
+            if (id >= 0 && id < r.n_b) {
+                const int64_t left = r.len - (((int64_t)id << p.g.c_log2) + w);
                 n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
-            } else if (g == 0 && t == 0) {
+            } else if (lane == 0) {
                 set_error(err, kErrBadId);
             }
         }
-        o.n[i] = n;
         if (n > 0) {  // the whole octet lies in the cache, even where only part of it is used
-            const int64_t ch = (chunk0 + id[i]) * p.g.Hkv + h;
-            const int64_t row = (ch << p.g.c_log2) + w;
+            const int64_t ch = (r.chunk0 + id) * p.g.Hkv + r.h;
+            const int64_t at = ((ch << p.g.c_log2) + w) * kDh + lane * 16;
+            const int row = lane >> 3, unit = lane & 7;
+            const uint32_t d0 = slot + (8 * i + row) * kDh + ((unit ^ row) << 4);
+            const uint32_t d1 = slot + (8 * i + row + 4) * kDh + ((unit ^ (row + 4)) << 4);
+            cp_async16(d0 + kKv8SlotK, p.K8 + at);
+            cp_async16(d1 + kKv8SlotK, p.K8 + at + 512);
+            cp_async16(d0 + kKv8SlotV, p.V8 + at);
+            cp_async16(d1 + kKv8SlotV, p.V8 + at + 512);
             const int64_t si = ch * p.g.spc + (w >> p.g.sb_log2);
-            const uint4 a = kv8_ld16(p.K8 + (row + g) * kDh + t * 32);
-            const uint4 b = kv8_ld16(p.K8 + (row + g) * kDh + t * 32 + 16);
-            o.v[2 * i] = kv8_ld16(p.V8 + (row + 2 * t) * kDh + g * 16);
-            o.v[2 * i + 1] = kv8_ld16(p.V8 + (row + 2 * t + 1) * kDh + g * 16);
-            o.ks[i] = p.k_scale[si];
-            o.vs[i] = p.v_scale[si];
-            o.k[i][0] = a.x; o.k[i][1] = a.y; o.k[i][2] = a.z; o.k[i][3] = a.w;
-            o.k[i][4] = b.x; o.k[i][5] = b.y; o.k[i][6] = b.z; o.k[i][7] = b.w;
-            if (n < 8) {  // rows behind the sequence may hold anything: a weight of 0 does not undo a NaN
-                const uint4 z = make_uint4(0, 0, 0, 0);
-                if (2 * t >= n) o.v[2 * i] = z;
-                if (2 * t + 1 >= n) o.v[2 * i + 1] = z;
-            }
-        } else {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            o.v[2 * i] = o.v[2 * i + 1] = z;
-            o.ks[i] = o.vs[i] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o.k[i][e] = 0;
+            if (lane < 2) cp_async4(slot + kKv8SlotMeta + 8 * lane + 4 * i, (lane ? p.v_scale : p.k_scale) + si);
         }
+        if (lane == 0)
+            asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + kKv8SlotMeta + 16 + 4 * i), "r"(n) : "memory");
     }
 }
 
@@ -152,12 +160,20 @@ __device__ __forceinline__ void kv8_load(Kv8Octets& o, const Kv8AttnParams& p, i
 template <bool QLO, bool PLO>
 __global__ void __launch_bounds__(kKv8Threads, kKv8CtasPerSm)
 k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
-    __shared__ float s_o[kKv8Warps][kKv8MaxRows][kDh];
-    __shared__ float s_ml[kKv8Warps][kKv8MaxRows][2];
+    extern __shared__ __align__(128) uint8_t smem[];
+    // the join's buffers take the ring's place once a run's tiles are done
+    float(*s_o)[kKv8MaxRows][kDh] = reinterpret_cast<float(*)[kKv8MaxRows][kDh]>(smem);
+    float(*s_ml)[kKv8MaxRows][2] =
+        reinterpret_cast<float(*)[kKv8MaxRows][2]>(smem + kKv8Warps * kKv8MaxRows * kDh * 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int64_t u0 = (int64_t)blockIdx.x * p.F / p.G, u1 = ((int64_t)blockIdx.x + 1) * p.F / p.G;
     const int runs_b = p.g.Hkv * p.rts;
     const int my_row = g & (p.rows - 1);
+    const uint32_t ring = smem_u32(smem) + warp * kKv8WarpBytes;
+    // byte offsets of this lane's fragments in a slot (second octet: + 8 rows)
+    const uint32_t k_at0 = g * kDh + ((2 * t ^ g) << 4), k_at1 = g * kDh + (((2 * t + 1) ^ g) << 4);
+    const uint32_t v_at0 = kKv8SlotV + 2 * t * kDh + ((g ^ 2 * t) << 4);
+    const uint32_t v_at1 = kKv8SlotV + (2 * t + 1) * kDh + ((g ^ (2 * t + 1)) << 4);
     pdl_trigger();
     pdl_wait();
 
@@ -179,13 +195,15 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         const int tile0 = (int)(rel - (int64_t)run * tiles);
         const int tile1 = (int)min((int64_t)tiles, tile0 + (u1 - u));
         const int h = run / p.rts, rt = run - h * p.rts;
-        const int n_b = tab.chunk_off[b + 1] - tab.chunk_off[b];
-        const int64_t chunk0 = tab.chunk_off[b];
-        int kept = tab.kept_off[b + 1] - tab.kept_off[b];
-        const int32_t* ids = p.ids != nullptr ? p.ids + tab.kept_off[b] : nullptr;
-        if (p.counts != nullptr) kept = max(0, min(kept, p.counts[b]));
-        int64_t len = (int64_t)n_b << p.g.c_log2;
-        if (p.seq_len != nullptr) len = min(len, (int64_t)p.seq_len[b] + p.len_add);
+        Kv8Run r;
+        r.h = h;
+        r.n_b = tab.chunk_off[b + 1] - tab.chunk_off[b];
+        r.chunk0 = tab.chunk_off[b];
+        r.kept = tab.kept_off[b + 1] - tab.kept_off[b];
+        r.ids = p.ids != nullptr ? p.ids + tab.kept_off[b] : nullptr;
+        if (p.counts != nullptr) r.kept = max(0, min(r.kept, p.counts[b]));
+        r.len = (int64_t)r.n_b << p.g.c_log2;
+        if (p.seq_len != nullptr) r.len = min(r.len, (int64_t)p.seq_len[b] + p.len_add);
         const int qrow0 = b * p.H + (h * p.rts + rt) * p.rows;
 
         // ---- q: 32 values of row my_row, scaled by a power of two, as f16 operands
@@ -239,37 +257,65 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-        for (int tile = tile0 + warp; tile < tile1; tile += kKv8Warps) {
-            Kv8Octets x;
-            {
-                int id[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = (tile * kKv8Tile + 8 * i) >> p.g.c_log2;
-                    id[i] = j >= kept ? -1 : ids != nullptr ? ids[j] : j;
+        // This warp's tiles are tile0 + warp + 4 i, i < n_it. Lane i holds the chunk ids of its tiles i,
+        // i + 32, ...: one load serves 32 tiles.
+        const int n_it = (tile1 - tile0 - warp + kKv8Warps - 1) / kKv8Warps;
+        int idv0 = 0, idv1 = 0;
+        auto issue = [&](int i) {
+            if (i < n_it) {
+                const int first = tile0 + warp + kKv8Warps * i;
+                if ((i & 31) == 0) {
+                    const int64_t tk = (int64_t)(first + kKv8Warps * lane) * kKv8Tile;
+                    const int64_t j0 = tk >> p.g.c_log2, j1 = (tk + 8) >> p.g.c_log2;
+                    idv0 = j0 >= r.kept ? -1 : r.ids != nullptr ? r.ids[j0] : (int)j0;
+                    idv1 = j1 >= r.kept ? -1 : r.ids != nullptr ? r.ids[j1] : (int)j1;
                 }
-                kv8_load(x, p, chunk0, n_b, h, kept, len, tile * kKv8Tile, id, g, t, err);
+                const int id0 = __shfl_sync(0xffffffffu, idv0, i & 31), id1 = __shfl_sync(0xffffffffu, idv1, i & 31);
+                kv8_issue(ring + (i % kKv8Stages) * kKv8SlotBytes, p, r, first * kKv8Tile, id0, id1, lane, err);
             }
-            if (x.n[0] + x.n[1] == 0) continue;  // uniform in the warp
+            cp_async_commit();  // one group per tile, empty past the end
+        };
+#pragma unroll
+        for (int i = 0; i < kKv8Stages - 1; ++i) issue(i);
 
-            // ---- S: rows of q against the tile's tokens
+        for (int it = 0; it < n_it; ++it) {
+            cp_async_wait<kKv8Stages - 2>();
+            __syncwarp();  // every lane's copies of this tile have landed, and the last tile's reads are done
+            issue(it + kKv8Stages - 1);
+            const uint32_t slot = ring + (it % kKv8Stages) * kKv8SlotBytes;
+            int n[2];
+            float ks[2], vs[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                asm volatile("ld.shared.s32 %0, [%1];" : "=r"(n[i]) : "r"(slot + kKv8SlotMeta + 16 + 4 * i));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[i]) : "r"(slot + kKv8SlotMeta + 4 * i));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs[i]) : "r"(slot + kKv8SlotMeta + 8 + 4 * i));
+                if (n[i] == 0) vs[i] = 0.f;
+            }
+            if (n[0] + n[1] == 0) continue;  // uniform in the warp
+
+            // ---- S: rows of q against the tile's tokens, in two chains of four products
             float sc[4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint4 ka = kv8_lds16(slot + k_at0 + 8 * i * kDh), kb = kv8_lds16(slot + k_at1 + 8 * i * kDh);
+                const uint32_t kw[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
+                float c[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_f16(c, qa[s][0], QLO ? ql[QLO ? s : 0][0] : 0u, qa[s][1], QLO ? ql[QLO ? s : 0][1] : 0u,
-                            e4m3lo_f16x2(x.k[i][s]), e4m3hi_f16x2(x.k[i][s]));
-                const float f = qmul * x.ks[i];
-                sc[2 * i] = 2 * t < x.n[i] ? (QLO ? c[0] + c[2] : c[0]) * f : -INFINITY;
-                sc[2 * i + 1] = 2 * t + 1 < x.n[i] ? (QLO ? c[1] + c[3] : c[1]) * f : -INFINITY;
+                    mma_f16(s < 4 ? c : e, qa[s][0], QLO ? ql[QLO ? s : 0][0] : 0u, qa[s][1],
+                            QLO ? ql[QLO ? s : 0][1] : 0u, e4m3lo_f16x2(kw[s]), e4m3hi_f16x2(kw[s]));
+                const float f = qmul * ks[i];
+                const float s0 = QLO ? (c[0] + e[0]) + (c[2] + e[2]) : c[0] + e[0];
+                const float s1 = QLO ? (c[1] + e[1]) + (c[3] + e[3]) : c[1] + e[1];
+                sc[2 * i] = 2 * t < n[i] ? s0 * f : -INFINITY;
+                sc[2 * i + 1] = 2 * t + 1 < n[i] ? s1 * f : -INFINITY;
             }
             // ---- running maximum of row my_row, and V's reference scale
             float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float vtop = fmaxf(x.vs[0], x.vs[1]);
+            const float vtop = fmaxf(vs[0], vs[1]);
             if (__any_sync(0xffffffffu, mx > m) || vtop > vref) {
                 const float mn = fmaxf(m, mx);
                 const float al = mn == -INFINITY ? 1.f : kv8_ex2(m - mn);
@@ -298,7 +344,7 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             for (int i = 0; i < 2; ++i) {
                 const float p0 = kv8_ex2(sc[2 * i] - ms), p1 = kv8_ex2(sc[2 * i + 1] - ms);
                 l += p0 + p1;
-                const float rv = x.vs[i] * inv_vref;
+                const float rv = vs[i] * inv_vref;
                 const float w0 = p0 * rv, w1 = p1 * rv;
                 ph[i] = f16x2_rn(w0, w1);
                 const float2 f = f16x2_floats(ph[i]);
@@ -306,10 +352,17 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                 if (!PLO && g >= 4) ph[i] = pl[i];  // columns 4..7 carry the low halves of columns 0..3
             }
             // ---- O^T += V^T P^T
-            const uint32_t* v0 = &x.v[0].x;
-            const uint32_t* v1 = &x.v[1].x;
-            const uint32_t* v2 = &x.v[2].x;
-            const uint32_t* v3 = &x.v[3].x;
+            uint4 vv[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                vv[2 * i] = kv8_lds16(slot + v_at0 + 8 * i * kDh);
+                vv[2 * i + 1] = kv8_lds16(slot + v_at1 + 8 * i * kDh);
+                if (n[i] < 8) {  // rows behind the sequence may hold anything: a weight of 0 does not undo a NaN
+                    if (2 * t >= n[i]) vv[2 * i] = make_uint4(0, 0, 0, 0);
+                    if (2 * t + 1 >= n[i]) vv[2 * i + 1] = make_uint4(0, 0, 0, 0);
+                }
+            }
+            const uint32_t *v0 = &vv[0].x, *v1 = &vv[1].x, *v2 = &vv[2].x, *v3 = &vv[3].x;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
 #pragma unroll
@@ -325,6 +378,8 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         }
 
         // ---- join the warps
+        cp_async_wait<0>();
+        __syncthreads();  // the rings are done with
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if constexpr (!PLO) {
@@ -468,7 +523,11 @@ cudaError_t kv8_init_attrs(int num_sms, int* ctas) {
                               (const void*)k_kv8_attn<true, false>, (const void*)k_kv8_attn<true, true>};
     for (const void* k : kernels) {
         int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kKv8Threads, 0);
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kKv8Smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     (int)cudaSharedmemCarveoutMaxShared);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kKv8Threads, kKv8Smem);
         if (e != cudaSuccess) return e;
         if (occ == 0 || n < occ) occ = n;
     }
@@ -546,6 +605,7 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     cfg.numAttrs = pdl ? 1 : 0;
     cfg.gridDim = dim3(p.G, 1, 1);
     cfg.blockDim = dim3(kKv8Threads, 1, 1);
+    cfg.dynamicSmemBytes = kKv8Smem;
     const bool qlo = d.kv_dtype != LSA_BF16, plo = p.rows > 4;
     cudaError_t e = qlo ? (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<true, true>, p, kt, err)
                                : cudaLaunchKernelEx(&cfg, k_kv8_attn<true, false>, p, kt, err))
@@ -555,6 +615,7 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     cfg.numAttrs = 1;  // the merge always follows the split kernel: overlap its launch
     cfg.gridDim = dim3(p.G, p.rows, 4);
     cfg.blockDim = dim3(kKv8MergeThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k_kv8_attn_merge, p, kt);
 }
 
