@@ -4,41 +4,53 @@
 //
 // for one decode query per sequence, H query heads sharing Hkv K/V heads in groups of H / Hkv.
 //
-// What bounds it: reading 2 Dh bytes a token and K/V head. Converting 8-bit codes and multiplying them
-// on the CUDA cores would take several instructions a byte, so both products run on the tensor cores
-// in f16 (m16n8k16): an e4m3 code is an f16 number exactly, and one conversion unpacks two. The
-// products are a few rows wide (one group of query heads), far from what fills a tcgen05 tile; the
-// warp-level instruction takes its operands from registers, where the loads put them.
+// What bounds it: reading 2 Dh bytes a token and K/V head, as long as the instructions spent on them
+// stay few. On the CUDA cores a byte would cost a conversion and a multiply-add; both products
+// therefore run on the tensor cores. They are one group of query heads wide, far from what fills a
+// tcgen05 tile, so they use the warp-level instructions, whose operands come from registers.
 //
-//  * Fragments straight from memory. The reduction index of a product may be permuted as long as both
-//    operands agree, so each lane loads whole 16- or 32-byte pieces and uses them as they come:
-//      S = q K^T   lane (g, t) of a warp (g = lane / 4, t = lane % 4) holds bytes 32 t .. 32 t + 31 of
-//                  token g's row: step s of the 8 steps over Dh takes its bytes 4 s .. 4 s + 3;
-//      O^T = V^T P^T  lane (g, t) holds bytes 16 g .. 16 g + 15 of tokens 2 t and 2 t + 1: interleaving
-//                  the two tokens' bytes (one byte permute per four) gives the pairs along the tokens.
-//    S leaves its scores exactly where the second product wants P, so nothing is exchanged between.
-//  * Full precision from f16 operands. A row of q is scaled by a power of two and, for fp32 queries,
-//    split into the f16 numbers hi + lo; lo sits in the eight rows of the 16-row operand that a group
-//    of up to 8 heads leaves free. The weights P, at most 2^14, are split in the same way: with 4 heads
-//    or fewer, lo takes the free half of the 8 columns (no extra product), with 8 heads a second
-//    product. Weights keep 22 bits down to 2^-28 of the largest and reach down to 2^-39.
+//  * S = q K^T takes the codes as they are (m16n8k32, e4m3). A row of q, scaled by a power of two, is
+//    split into e4m3 terms of four bits each, term i worth 16^-i: two terms hold a bf16 number, six an
+//    fp32 one. The terms lie in the rows of the 16-row operand that a group of up to 8 heads leaves
+//    free: two terms cost nothing extra, six cost three products. (The same product in f16, with a
+//    conversion per two codes, took 48 more instructions per 16 tokens.)
+//  * O^T = V^T P^T runs in f16 (m16n8k16), for the weights P need more bits than e4m3 terms would give
+//    cheaply. An e4m3 code is an f16 number exactly. P, at most 2^14, is split into f16 hi + lo: with
+//    4 heads or fewer lo takes the free half of the 8 columns, with 8 heads a second product. Weights
+//    keep 22 bits down to 2^-28 of the largest and reach down to 2^-39.
+//  * The reduction index of a product may be permuted as long as both operands agree, so each lane uses
+//    whole 16-byte pieces as they come. Lane (g, t) of a warp (g = lane / 4, t = lane % 4) takes bytes
+//    32 t .. 32 t + 31 of token g's row of K; and bytes 16 g .. 16 g + 15 of tokens 2 t and 2 t + 1 of V,
+//    whose bytes a permute interleaves into pairs along the tokens. S leaves its scores exactly where
+//    the second product wants P, so nothing is exchanged between them.
 //  * V's scale multiplies the weight, relative to the largest scale seen (vref), which the running
 //    output carries, so that the products stay within f16's range whatever the scales are.
-//  * The cache's (chunk, head) runs are contiguous; each warp streams tiles of 16 tokens of one
-//    (sequence, K/V head) run, with its own running maximum, sum and output. The tiles of all runs form
-//    one list that is split evenly over the CTAs; a CTA joins its warps in shared memory, and a run that
-//    spans CTAs is joined by k_kv8_attn_merge. Runs that one CTA holds whole are written at once.
+//  * The tensor cores truncate when they accumulate: each tile's product starts from zero and is added
+//    to the running output in fp32, rounded to nearest, by the multiply-add that also rescales it.
+//  * A warp streams tiles of 32 tokens of one (sequence, K/V head) run through its own two-slot ring in
+//    shared memory, filled by asynchronous copies (no barrier between warps); K's half of a slot is
+//    refilled as soon as S is done, V's after the second product: 96 KB in flight per SM. What it has
+//    to know of a tile (chunk id, row, scales, how many tokens exist) its lanes work out side by side
+//    for 32 groups of 8 tokens ("octets") at a time.
+//  * The tiles of all runs form one list that is split evenly over the CTAs; a CTA joins its warps in
+//    shared memory, and a run that spans CTAs is joined by k_kv8_attn_merge. Runs that one CTA holds
+//    whole are written at once.
 #include "kv8.cuh"
 
 namespace lsa {
 
 constexpr int kKv8Warps = 4;
 constexpr int kKv8Threads = kKv8Warps * 32;
-constexpr int kKv8CtasPerSm = 3;
-constexpr int kKv8Stages = 4;      // tiles of a warp's ring
-constexpr int kKv8Tile = 16;       // tokens per tile
+constexpr int kKv8Tile = 32;       // tokens per tile: 4 octets
+constexpr int kKv8Batch = 8;       // tiles whose 32 octets the lanes hold
 constexpr int kKv8MaxRows = 8;     // query heads per run
 constexpr float kKv8PShift = 14.f; // weights are at most 2^14
+constexpr int kKv8SlotBytes = 2 * kKv8Tile * kDh;  // K rows, then V rows
+constexpr int kKv8SlotV = kKv8Tile * kDh;
+constexpr int kKv8WarpBytes = 2 * kKv8SlotBytes;
+constexpr int kKv8JoinBytes = kKv8Warps * kKv8MaxRows * (kDh + 2) * 4;  // takes the rings' place
+constexpr int kKv8Smem = kKv8Warps * kKv8WarpBytes;
+static_assert(kKv8JoinBytes <= kKv8Smem, "the join's buffers lie in the rings");
 
 // Prefix tables of one call: the kept (or all) chunks and their tiles.
 struct Kv8Tab {
@@ -78,28 +90,21 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-// ---------------------------------------------------------------- a warp's ring of tiles
-// One slot: 16 rows of K, 16 rows of V (128 bytes each), then the tile's scales and token counts. A
-// row's 16-byte units are XOR-swizzled by the row, so that both fragment reads are free of conflicts.
-constexpr int kKv8SlotK = 0;
-constexpr int kKv8SlotV = kKv8Tile * kDh;
-constexpr int kKv8SlotMeta = 2 * kKv8Tile * kDh;  // ks[2], vs[2] (float), n[2] (int)
-constexpr int kKv8SlotBytes = kKv8SlotMeta + 32;
-constexpr int kKv8WarpBytes = kKv8Stages * kKv8SlotBytes;
-constexpr int kKv8JoinBytes = kKv8Warps * kKv8MaxRows * (kDh + 2) * 4;
-constexpr int kKv8Smem = kKv8Warps * kKv8WarpBytes > kKv8JoinBytes ? kKv8Warps * kKv8WarpBytes : kKv8JoinBytes;
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -112,56 +117,20 @@ __device__ __forceinline__ uint4 kv8_lds16(uint32_t addr) {
     return v;
 }
 
-// The run that a warp streams.
-struct Kv8Run {
-    int64_t chunk0;      // first chunk of the sequence
-    int64_t len;         // tokens of the sequence that exist
-    const int32_t* ids;  // nullable
-    int n_b, kept, h;
+// One lane's octet of a batch: its first row in the cache (in rows of Dh bytes), how many of its 8
+// tokens take part, its scales.
+struct Kv8Octet {
+    uint32_t row;
+    int n;
+    float ks, vs;
 };
 
-// Start the copies of one tile into `slot`: first token t0 within the run, the ids of its two octets'
-// chunks. The counts n are what the consumer goes by: an octet without tokens is not copied.
-__device__ __forceinline__ void kv8_issue(uint32_t slot, const Kv8AttnParams& p, const Kv8Run& r, int t0, int id0,
-                                          int id1, int lane, uint32_t* err) {
-    const int cm = (1 << p.g.c_log2) - 1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int tk = t0 + 8 * i, id = i ? id1 : id0;
-        const int j = tk >> p.g.c_log2, w = tk & cm;
-        int n = 0;
-        if (j < r.kept) {
-            if (id >= 0 && id < r.n_b) {
-                const int64_t left = r.len - (((int64_t)id << p.g.c_log2) + w);
-                n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
-            } else if (lane == 0) {
-                set_error(err, kErrBadId);
-            }
-        }
-        if (n > 0) {  // the whole octet lies in the cache, even where only part of it is used
-            const int64_t ch = (r.chunk0 + id) * p.g.Hkv + r.h;
-            const int64_t at = ((ch << p.g.c_log2) + w) * kDh + lane * 16;
-            const int row = lane >> 3, unit = lane & 7;
-            const uint32_t d0 = slot + (8 * i + row) * kDh + ((unit ^ row) << 4);
-            const uint32_t d1 = slot + (8 * i + row + 4) * kDh + ((unit ^ (row + 4)) << 4);
-            cp_async16(d0 + kKv8SlotK, p.K8 + at);
-            cp_async16(d1 + kKv8SlotK, p.K8 + at + 512);
-            cp_async16(d0 + kKv8SlotV, p.V8 + at);
-            cp_async16(d1 + kKv8SlotV, p.V8 + at + 512);
-            const int64_t si = ch * p.g.spc + (w >> p.g.sb_log2);
-            if (lane < 2) cp_async4(slot + kKv8SlotMeta + 8 * lane + 4 * i, (lane ? p.v_scale : p.k_scale) + si);
-        }
-        if (lane == 0)
-            asm volatile("st.shared.s32 [%0], %1;" ::"r"(slot + kKv8SlotMeta + 16 + 4 * i), "r"(n) : "memory");
-    }
-}
-
-// grid G, kKv8Threads threads. QLO: fp32 queries (hi + lo); PLO: groups of 8 (a second product for lo).
-template <bool QLO, bool PLO>
-__global__ void __launch_bounds__(kKv8Threads, kKv8CtasPerSm)
+// grid G, kKv8Threads threads. SETS: products of S, two terms of q each (bf16: 1, fp32: 3); PLO: groups
+// of 8 (a second product for P's low halves).
+template <int SETS, bool PLO>
+__global__ void __launch_bounds__(kKv8Threads, SETS == 1 ? 3 : 2)  // what the rings leave room for, and q's terms
 k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     extern __shared__ __align__(128) uint8_t smem[];
-    // the join's buffers take the ring's place once a run's tiles are done
     float(*s_o)[kKv8MaxRows][kDh] = reinterpret_cast<float(*)[kKv8MaxRows][kDh]>(smem);
     float(*s_ml)[kKv8MaxRows][2] =
         reinterpret_cast<float(*)[kKv8MaxRows][2]>(smem + kKv8Warps * kKv8MaxRows * kDh * 4);
@@ -169,8 +138,13 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     const int64_t u0 = (int64_t)blockIdx.x * p.F / p.G, u1 = ((int64_t)blockIdx.x + 1) * p.F / p.G;
     const int runs_b = p.g.Hkv * p.rts;
     const int my_row = g & (p.rows - 1);
+    const int c_log2 = p.g.c_log2;
+    const bool contig = c_log2 >= 5;  // a tile's octets follow one another in the cache
     const uint32_t ring = smem_u32(smem) + warp * kKv8WarpBytes;
-    // byte offsets of this lane's fragments in a slot (second octet: + 8 rows)
+    // A row's 16-byte units are XOR-swizzled by the row: the copies' and both fragments' accesses are
+    // free of bank conflicts. Offsets of this lane within an octet (8 rows, 1 KB):
+    const uint32_t cp0 = (lane >> 3) * kDh + (((lane & 7) ^ (lane >> 3)) << 4);
+    const uint32_t cp1 = ((lane >> 3) + 4) * kDh + (((lane & 7) ^ ((lane >> 3) + 4)) << 4);
     const uint32_t k_at0 = g * kDh + ((2 * t ^ g) << 4), k_at1 = g * kDh + (((2 * t + 1) ^ g) << 4);
     const uint32_t v_at0 = kKv8SlotV + 2 * t * kDh + ((g ^ 2 * t) << 4);
     const uint32_t v_at1 = kKv8SlotV + (2 * t + 1) * kDh + ((g ^ (2 * t + 1)) << 4);
@@ -195,191 +169,272 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         const int tile0 = (int)(rel - (int64_t)run * tiles);
         const int tile1 = (int)min((int64_t)tiles, tile0 + (u1 - u));
         const int h = run / p.rts, rt = run - h * p.rts;
-        Kv8Run r;
-        r.h = h;
-        r.n_b = tab.chunk_off[b + 1] - tab.chunk_off[b];
-        r.chunk0 = tab.chunk_off[b];
-        r.kept = tab.kept_off[b + 1] - tab.kept_off[b];
-        r.ids = p.ids != nullptr ? p.ids + tab.kept_off[b] : nullptr;
-        if (p.counts != nullptr) r.kept = max(0, min(r.kept, p.counts[b]));
-        r.len = (int64_t)r.n_b << p.g.c_log2;
-        if (p.seq_len != nullptr) r.len = min(r.len, (int64_t)p.seq_len[b] + p.len_add);
+        const int n_b = tab.chunk_off[b + 1] - tab.chunk_off[b];
+        int kept = tab.kept_off[b + 1] - tab.kept_off[b];
+        const int32_t* ids = p.ids != nullptr ? p.ids + tab.kept_off[b] : nullptr;
+        if (p.counts != nullptr) kept = max(0, min(kept, p.counts[b]));
+        int64_t len = (int64_t)n_b << c_log2;
+        if (p.seq_len != nullptr) len = max((int64_t)0, min(len, (int64_t)p.seq_len[b] + p.len_add));
+        if (ids == nullptr) kept = min(kept, (int)((len + (1 << c_log2) - 1) >> c_log2));
         const int qrow0 = b * p.H + (h * p.rts + rt) * p.rows;
+        // This warp's tiles are tile0 + warp + kKv8Warps * i, i < n_it, as far as there are tokens.
+        const int last = min(tile1, (int)((((int64_t)kept << c_log2) + kKv8Tile - 1) / kKv8Tile));
+        const int n_it = (max(last - tile0 - warp, 0) + kKv8Warps - 1) / kKv8Warps;
 
-        // ---- q: 32 values of row my_row, scaled by a power of two, as f16 operands
-        uint32_t qa[8][2], ql[QLO ? 8 : 1][2];
-        float qmul;
-        {
-            float x[32], top = 0.f;
-            const int64_t at = (int64_t)(qrow0 + my_row) * kDh + t * 32;
-            if constexpr (QLO) {
-                const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + at);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 f = src[e];
-                    x[4 * e] = f.x; x[4 * e + 1] = f.y; x[4 * e + 2] = f.z; x[4 * e + 3] = f.w;
-                }
-            } else {
-                const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + at);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint4 f = src[e];
-                    x[8 * e] = bf16lo(f.x); x[8 * e + 1] = bf16hi(f.x);
-                    x[8 * e + 2] = bf16lo(f.y); x[8 * e + 3] = bf16hi(f.y);
-                    x[8 * e + 4] = bf16lo(f.z); x[8 * e + 5] = bf16hi(f.z);
-                    x[8 * e + 6] = bf16lo(f.w); x[8 * e + 7] = bf16hi(f.w);
+        // ---- what the lanes know of the octets: lane L has octet L % 4 of tile (batch) + L / 4
+        Kv8Octet oct = {0, 0, 0.f, 0.f};  // of the tiles being copied
+        uint32_t nz = 0;                  // octets (lanes) with tokens
+        int id_next = 0;
+        auto token_of = [&](int i) {      // first token of this lane's octet in the batch of tile i
+            return (tile0 + warp + kKv8Warps * (i + (lane >> 2))) * kKv8Tile + 8 * (lane & 3);
+        };
+        auto fetch_id = [&](int i) {
+            const int j = token_of(i) >> c_log2;
+            id_next = j >= kept ? -1 : ids != nullptr ? ids[j] : j;
+        };
+        auto next_batch = [&](int i) {
+            const int tk = token_of(i), j = tk >> c_log2, w = tk & ((1 << c_log2) - 1), id = id_next;
+            oct.n = 0;
+            oct.ks = oct.vs = 0.f;
+            if (j < kept && i + (lane >> 2) < n_it) {
+                if (id >= 0 && id < n_b) {
+                    const int64_t left = len - (((int64_t)id << c_log2) + w);
+                    oct.n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+                    const int64_t ch = (int64_t)(tab.chunk_off[b] + id) * p.g.Hkv + h;
+                    oct.row = (uint32_t)((ch << c_log2) + w);
+                    if (oct.n > 0) {
+                        const int64_t si = ch * p.g.spc + (w >> p.g.sb_log2);
+                        oct.ks = p.k_scale[si];
+                        oct.vs = p.v_scale[si];
+                    }
+                } else {
+                    set_error(err, kErrBadId);
                 }
             }
+            nz = __ballot_sync(0xffffffffu, oct.n > 0);
+            fetch_id(i + kKv8Batch);
+        };
+        // Copies of tile i's K or V rows into its slot, one group for each (empty past the end). Octets
+        // without tokens are not copied; of the others all 8 rows are (they lie in the cache).
+        auto copy = [&](int i, const uint8_t* base, uint32_t off) {
+            if (i < n_it) {
+                const int l0 = 4 * (i & (kKv8Batch - 1));
+                const uint32_t dst = ring + (i & 1) * kKv8SlotBytes + off;
+                if (contig) {  // if the first octet has no tokens, the later ones have none either
+                    const uint32_t row = __shfl_sync(0xffffffffu, oct.row, l0);
+                    if (nz >> l0 & 1) {
+                        const uint8_t* src = base + (uint64_t)row * kDh + lane * 16;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, fabsf(x[e]));
+                        for (int o = 0; o < 4; ++o) {
+                            cp_async16(dst + cp0 + o * 8 * kDh, src + o * 8 * kDh);
+                            cp_async16(dst + cp1 + o * 8 * kDh, src + o * 8 * kDh + 4 * kDh);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int o = 0; o < 4; ++o) {
+                        const uint32_t row = __shfl_sync(0xffffffffu, oct.row, l0 + o);
+                        if (nz >> (l0 + o) & 1) {
+                            const uint8_t* src = base + (uint64_t)row * kDh + lane * 16;
+                            cp_async16(dst + cp0 + o * 8 * kDh, src);
+                            cp_async16(dst + cp1 + o * 8 * kDh, src + 4 * kDh);
+                        }
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+
+        fetch_id(0);
+        next_batch(0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            copy(i, p.K8, 0);
+            copy(i, p.V8, kKv8SlotV);
+        }
+
+        // ---- q: 32 values of row my_row, scaled to stay below 256, as e4m3 terms worth 16^-i
+        uint32_t qa[SETS][4][4];
+        float qmul;
+        {
+            const int64_t at = (int64_t)(qrow0 + my_row) * kDh + t * 32;
+            auto load = [&](int i, float* x) {  // values 8 i .. 8 i + 7 of the lane's 32
+                constexpr bool BF16 = SETS == 1;
+                octet_floats<BF16>(octet_load<BF16>(p.q + at * (BF16 ? 2 : 4), i), x);
+            };
+            float top = 0.f;
+            bool nan = false;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float x[8];
+                load(s, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    top = fmaxf(top, fabsf(x[e]));
+                    nan |= x[e] != x[e];
+                }
+            }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // top < 2^(ex + 1): times 2^(14 - ex) it stays below 2^15. The factor is kept within fp32.
+            // top < 2^(ex + 1): times 2^(7 - ex) it stays below 2^8. The factor is kept within fp32.
             int ex = (int)(__float_as_uint(top) >> 23) - 127;
-            ex = ex < -100 ? -100 : ex > 127 ? 127 : ex;
-            const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-            qmul = p.qscale * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+            ex = ex < -110 ? -110 : ex;
+            const float up = __uint_as_float((uint32_t)(7 - ex + 127) << 23);
+            qmul = p.qscale * __uint_as_float((uint32_t)(ex - 7 + 127) << 23);
+            // a row with an infinity or a NaN has no finite scores
+            const uint32_t bad = __ballot_sync(0xffffffffu, nan || !(top < INFINITY));
+            if (bad >> (lane & 28) & 15) qmul = __uint_as_float(0x7fc00000u);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int s = 0; s < 4; ++s) {
+                float y[8];
+                load(s, y);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float a = x[4 * e + 2 * i] * up, c = x[4 * e + 2 * i + 1] * up;
-                    qa[e][i] = f16x2_rn(a, c);
-                    if constexpr (QLO) {
-                        const float2 f = f16x2_floats(qa[e][i]);
-                        ql[e][i] = f16x2_rn(a - f.x, c - f.y);
+                for (int e = 0; e < 8; ++e) y[e] *= up;
+#pragma unroll
+                for (int k = 0; k < 2 * SETS; ++k) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w = e4m3x4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                        qa[k >> 1][s][2 * i + (k & 1)] = w;
+                        float f[4];
+                        e4m3x4_floats(w, f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[4 * i + e] = (y[4 * i + e] - f[e]) * 16.f;
                     }
                 }
             }
         }
 
-        float o[8][4], m = -INFINITY, l = 0.f, vref = 0.f, inv_vref = 0.f;
+        float o[8][4], m = -INFINITY, l = 0.f, vref = 0.f;
+        float rv = 0.f, ks = 0.f;  // this lane's octet of the batch being read: vs / vref and ks
+        uint32_t full = 0;         // octets whose 8 tokens all take part
+        int n = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-        // This warp's tiles are tile0 + warp + 4 i, i < n_it. Lane i holds the chunk ids of its tiles i,
-        // i + 32, ...: one load serves 32 tiles.
-        const int n_it = (tile1 - tile0 - warp + kKv8Warps - 1) / kKv8Warps;
-        int idv0 = 0, idv1 = 0;
-        auto issue = [&](int i) {
-            if (i < n_it) {
-                const int first = tile0 + warp + kKv8Warps * i;
-                if ((i & 31) == 0) {
-                    const int64_t tk = (int64_t)(first + kKv8Warps * lane) * kKv8Tile;
-                    const int64_t j0 = tk >> p.g.c_log2, j1 = (tk + 8) >> p.g.c_log2;
-                    idv0 = j0 >= r.kept ? -1 : r.ids != nullptr ? r.ids[j0] : (int)j0;
-                    idv1 = j1 >= r.kept ? -1 : r.ids != nullptr ? r.ids[j1] : (int)j1;
-                }
-                const int id0 = __shfl_sync(0xffffffffu, idv0, i & 31), id1 = __shfl_sync(0xffffffffu, idv1, i & 31);
-                kv8_issue(ring + (i % kKv8Stages) * kKv8SlotBytes, p, r, first * kKv8Tile, id0, id1, lane, err);
-            }
-            cp_async_commit();  // one group per tile, empty past the end
-        };
-#pragma unroll
-        for (int i = 0; i < kKv8Stages - 1; ++i) issue(i);
-
         for (int it = 0; it < n_it; ++it) {
-            cp_async_wait<kKv8Stages - 2>();
-            __syncwarp();  // every lane's copies of this tile have landed, and the last tile's reads are done
-            issue(it + kKv8Stages - 1);
-            const uint32_t slot = ring + (it % kKv8Stages) * kKv8SlotBytes;
-            int n[2];
-            float ks[2], vs[2];
+            const uint32_t slot = ring + (it & 1) * kKv8SlotBytes;
+            const int l0 = 4 * (it & (kKv8Batch - 1));
+            float vf = 1.f;
+            if (l0 == 0) {  // a new batch: its scales, and V's reference
+                n = oct.n;
+                ks = oct.ks;
+                full = __ballot_sync(0xffffffffu, n == 8);
+                float vtop = oct.vs;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                asm volatile("ld.shared.s32 %0, [%1];" : "=r"(n[i]) : "r"(slot + kKv8SlotMeta + 16 + 4 * i));
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[i]) : "r"(slot + kKv8SlotMeta + 4 * i));
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs[i]) : "r"(slot + kKv8SlotMeta + 8 + 4 * i));
-                if (n[i] == 0) vs[i] = 0.f;
+                for (int k = 1; k < 32; k <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, k));
+                if (vtop > vref && vtop >= 1.17549435e-38f) {
+                    vf = vref / vtop;
+                    vref = vtop;
+                }
+                rv = vref > 0.f ? oct.vs / vref : 0.f;
             }
-            if (n[0] + n[1] == 0) continue;  // uniform in the warp
+            const bool whole = (full >> l0 & 15u) == 15u;
 
-            // ---- S: rows of q against the tile's tokens, in two chains of four products
-            float sc[4];
+            // ---- S: the terms of q against the tile's tokens
+            cp_async_wait<3>();
+            __syncwarp();  // every lane's copies of these rows have landed
+            float sc[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 ka = kv8_lds16(slot + k_at0 + 8 * i * kDh), kb = kv8_lds16(slot + k_at1 + 8 * i * kDh);
+            for (int i = 0; i < 4; ++i) {
+                const uint4 ka = kv8_lds16(slot + k_at0 + i * 8 * kDh), kb = kv8_lds16(slot + k_at1 + i * 8 * kDh);
                 const uint32_t kw[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
-                float c[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_f16(s < 4 ? c : e, qa[s][0], QLO ? ql[QLO ? s : 0][0] : 0u, qa[s][1],
-                            QLO ? ql[QLO ? s : 0][1] : 0u, e4m3lo_f16x2(kw[s]), e4m3hi_f16x2(kw[s]));
-                const float f = qmul * ks[i];
-                const float s0 = QLO ? (c[0] + e[0]) + (c[2] + e[2]) : c[0] + e[0];
-                const float s1 = QLO ? (c[1] + e[1]) + (c[3] + e[3]) : c[1] + e[1];
-                sc[2 * i] = 2 * t < n[i] ? s0 * f : -INFINITY;
-                sc[2 * i + 1] = 2 * t + 1 < n[i] ? s1 * f : -INFINITY;
+                for (int k = SETS - 1; k >= 0; --k) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) mma_e4m3(c, qa[k][s], kw[2 * s], kw[2 * s + 1]);
+                    s0 = fmaf(fmaf(s0, 0.0625f, c[2]), 0.0625f, c[0]);
+                    s1 = fmaf(fmaf(s1, 0.0625f, c[3]), 0.0625f, c[1]);
+                }
+                const float f = qmul * __shfl_sync(0xffffffffu, ks, l0 + i);
+                sc[2 * i] = s0 * f;
+                sc[2 * i + 1] = s1 * f;
             }
-            // ---- running maximum of row my_row, and V's reference scale
-            float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int ni = __shfl_sync(0xffffffffu, n, l0 + i);
+                    if (2 * t >= ni) sc[2 * i] = -INFINITY;
+                    if (2 * t + 1 >= ni) sc[2 * i + 1] = -INFINITY;
+                }
+            }
+            __syncwarp();  // the slot's K rows are read
+            if ((it + 2) % kKv8Batch == 0) next_batch(it + 2);
+            copy(it + 2, p.K8, 0);
+
+            // ---- running maximum of row my_row
+            float mx = m;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx = fmaxf(mx, sc[i]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float vtop = fmaxf(vs[0], vs[1]);
-            if (__any_sync(0xffffffffu, mx > m) || vtop > vref) {
-                const float mn = fmaxf(m, mx);
-                const float al = mn == -INFINITY ? 1.f : kv8_ex2(m - mn);
-                m = mn;
-                l *= al;
-                float a0 = __shfl_sync(0xffffffffu, al, 8 * t), a1 = __shfl_sync(0xffffffffu, al, 8 * t + 4);
-                if (vtop > vref && vtop >= 1.17549435e-38f) {
-                    const float f = vref / vtop;
-                    a0 *= f;
-                    a1 *= f;
-                    vref = vtop;
-                    inv_vref = 1.f / vtop;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    o[j][0] *= a0;
-                    o[j][1] *= a1;
-                    o[j][2] *= a0;
-                    o[j][3] *= a1;
-                }
-            }
+            const float ref = mx == -INFINITY ? 0.f : mx;
+            const float al = kv8_ex2(m - ref);
+            m = mx;
+            const float a0 = __shfl_sync(0xffffffffu, al, 8 * t) * vf;  // of columns 2 t and 2 t + 1
+            const float a1 = __shfl_sync(0xffffffffu, al, 8 * t + 4) * vf;
             // ---- weights (times 2^14, which out = O / l cancels) and their f16 halves
-            const float ms = m == -INFINITY ? 0.f : m - kKv8PShift;
-            uint32_t ph[2], pl[2];
+            const float ms = ref - kKv8PShift;
+            uint32_t ph[4], pl[PLO ? 4 : 1];
+            l *= al;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 const float p0 = kv8_ex2(sc[2 * i] - ms), p1 = kv8_ex2(sc[2 * i + 1] - ms);
                 l += p0 + p1;
-                const float rv = vs[i] * inv_vref;
-                const float w0 = p0 * rv, w1 = p1 * rv;
+                const float r = __shfl_sync(0xffffffffu, rv, l0 + i);
+                const float w0 = p0 * r, w1 = p1 * r;
                 ph[i] = f16x2_rn(w0, w1);
                 const float2 f = f16x2_floats(ph[i]);
-                pl[i] = f16x2_rn(w0 - f.x, w1 - f.y);
-                if (!PLO && g >= 4) ph[i] = pl[i];  // columns 4..7 carry the low halves of columns 0..3
+                const uint32_t low = f16x2_rn(w0 - f.x, w1 - f.y);
+                if constexpr (PLO) pl[i] = low;
+                else if (g >= 4) ph[i] = low;  // columns 4..7 carry the low halves of columns 0..3
             }
-            // ---- O^T += V^T P^T
-            uint4 vv[4];
+
+            // ---- O^T = O^T alpha + V^T P^T
+            cp_async_wait<3>();
+            __syncwarp();
+            uint4 vv[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                vv[2 * i] = kv8_lds16(slot + v_at0 + 8 * i * kDh);
-                vv[2 * i + 1] = kv8_lds16(slot + v_at1 + 8 * i * kDh);
-                if (n[i] < 8) {  // rows behind the sequence may hold anything: a weight of 0 does not undo a NaN
-                    if (2 * t >= n[i]) vv[2 * i] = make_uint4(0, 0, 0, 0);
-                    if (2 * t + 1 >= n[i]) vv[2 * i + 1] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 4; ++i) {
+                vv[2 * i] = kv8_lds16(slot + v_at0 + i * 8 * kDh);
+                vv[2 * i + 1] = kv8_lds16(slot + v_at1 + i * 8 * kDh);
+            }
+            if (!whole) {  // rows behind the sequence may hold anything: a weight of 0 does not undo a NaN
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int ni = __shfl_sync(0xffffffffu, n, l0 + i);
+                    if (2 * t >= ni) vv[2 * i] = make_uint4(0, 0, 0, 0);
+                    if (2 * t + 1 >= ni) vv[2 * i + 1] = make_uint4(0, 0, 0, 0);
                 }
             }
-            const uint32_t *v0 = &vv[0].x, *v1 = &vv[1].x, *v2 = &vv[2].x, *v3 = &vv[3].x;
+            __syncwarp();  // the slot's V rows are read
+            copy(it + 2, p.V8, kKv8SlotV);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t y0 = __byte_perm(v0[w], v1[w], i ? 0x7362 : 0x5140);
-                    const uint32_t y1 = __byte_perm(v2[w], v3[w], i ? 0x7362 : 0x5140);
-                    const uint32_t a0 = e4m3lo_f16x2(y0), a1 = e4m3hi_f16x2(y0);
-                    const uint32_t a2 = e4m3lo_f16x2(y1), a3 = e4m3hi_f16x2(y1);
-                    mma_f16(o[2 * w + i], a0, a1, a2, a3, ph[0], ph[1]);
-                    if constexpr (PLO) mma_f16(o[2 * w + i], a0, a1, a2, a3, pl[0], pl[1]);
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {  // tokens 0..15, 16..31 of the tile
+                        const uint32_t y0 = __byte_perm((&vv[4 * e].x)[w], (&vv[4 * e + 1].x)[w], i ? 0x7362 : 0x5140);
+                        const uint32_t y1 = __byte_perm((&vv[4 * e + 2].x)[w], (&vv[4 * e + 3].x)[w], i ? 0x7362 : 0x5140);
+                        const uint32_t b0 = e4m3lo_f16x2(y0), b1 = e4m3hi_f16x2(y0);
+                        const uint32_t b2 = e4m3lo_f16x2(y1), b3 = e4m3hi_f16x2(y1);
+                        mma_f16(c, b0, b1, b2, b3, ph[2 * e], ph[2 * e + 1]);
+                        if constexpr (PLO) mma_f16(c, b0, b1, b2, b3, pl[2 * e], pl[2 * e + 1]);
+                    }
+                    float(&oo)[4] = o[2 * w + i];
+                    oo[0] = fmaf(oo[0], a0, c[0]);
+                    oo[1] = fmaf(oo[1], a1, c[1]);
+                    oo[2] = fmaf(oo[2], a0, c[2]);
+                    oo[3] = fmaf(oo[3], a1, c[3]);
                 }
             }
         }
 
         // ---- join the warps
-        cp_async_wait<0>();
-        __syncthreads();  // the rings are done with
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if constexpr (!PLO) {
@@ -388,6 +443,8 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[j][e] += __shfl_xor_sync(0xffffffffu, o[j][e], 2);
         }
+        cp_async_wait<0>();
+        __syncthreads();  // the rings are done with
         if (t == 0 && g < p.rows) {
             s_ml[warp][g][0] = m == -INFINITY ? -INFINITY : m - kKv8PShift;
             s_ml[warp][g][1] = l;
@@ -404,7 +461,7 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             }
         }
         __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == tiles;
+        const bool all = tile0 == 0 && tile1 == tiles;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1);
         for (int i = tid; i < p.rows * kDh; i += kKv8Threads) {
             const int row = i >> 7, d = i & (kDh - 1);
@@ -418,10 +475,10 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                 A = fmaf(f, s_o[w][row][d], A);
                 L = fmaf(f, s_ml[w][row][1], L);
             }
-            if (whole) {
-                p.out[(int64_t)(qrow0 + row) * kDh + d] = M == -INFINITY ? 0.f : A / L;
+            if (all) {
+                p.out[(int64_t)(qrow0 + row) * kDh + d] = L == 0.f ? 0.f : A / L;
                 if (d == 0 && p.lse != nullptr)
-                    p.lse[qrow0 + row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+                    p.lse[qrow0 + row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
             } else {
                 p.part_o[(slot * kKv8MaxRows + row) * kDh + d] = A;
                 if (d == 0) {
@@ -512,26 +569,29 @@ k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab) {
     }
     const int h = run / p.rts, rt = run - h * p.rts;
     const int q = b * p.H + (h * p.rts + rt) * p.rows + row;
-    p.out[(int64_t)q * kDh + d] = M == -INFINITY ? 0.f : A / L;
-    if (d == 0 && p.lse != nullptr) p.lse[q] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    p.out[(int64_t)q * kDh + d] = L == 0.f ? 0.f : A / L;
+    if (d == 0 && p.lse != nullptr) p.lse[q] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host side
+// CTAs that the device holds at once, per kv_dtype (LSA_F32, LSA_BF16); the kernels' attributes.
 cudaError_t kv8_init_attrs(int num_sms, int* ctas) {
-    int occ = 0;  // the least of the variants': one split serves them all
-    const void* kernels[4] = {(const void*)k_kv8_attn<false, false>, (const void*)k_kv8_attn<false, true>,
-                              (const void*)k_kv8_attn<true, false>, (const void*)k_kv8_attn<true, true>};
-    for (const void* k : kernels) {
-        int n = 0;
-        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kKv8Smem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                     (int)cudaSharedmemCarveoutMaxShared);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kKv8Threads, kKv8Smem);
-        if (e != cudaSuccess) return e;
-        if (occ == 0 || n < occ) occ = n;
+    const void* kernels[2][2] = {{(const void*)k_kv8_attn<3, false>, (const void*)k_kv8_attn<3, true>},
+                                 {(const void*)k_kv8_attn<1, false>, (const void*)k_kv8_attn<1, true>}};
+    for (int dt = 0; dt < 2; ++dt) {
+        int occ = 0;
+        for (const void* k : kernels[dt]) {
+            int n = 0;
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kKv8Smem);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         (int)cudaSharedmemCarveoutMaxShared);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kKv8Threads, kKv8Smem);
+            if (e != cudaSuccess) return e;
+            if (occ == 0 || n < occ) occ = n;
+        }
+        ctas[dt] = (occ < 1 ? 1 : occ) * num_sms;
     }
-    *ctas = (occ < 1 ? 1 : occ) * num_sms;
     return cudaSuccess;
 }
 
@@ -588,9 +648,9 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     const int runs_b = g.Hkv * p.rts;
     const int64_t runs = (int64_t)runs_b * tab.B;
     p.F = tiles * runs_b;
-    // Few tiles: at least four to a warp, one CTA to a run if that is enough, so that nothing is left
+    // Few tiles: at least two to a warp, one CTA to a run if that is enough, so that nothing is left
     // to join; many: every resident CTA an equal share.
-    int64_t G = (p.F + 4 * kKv8Warps - 1) / (4 * kKv8Warps);
+    int64_t G = (p.F + 2 * kKv8Warps - 1) / (2 * kKv8Warps);
     if (G < runs) G = runs;
     if (G > max_ctas) G = max_ctas;
     if (G > p.F) G = p.F;
@@ -606,11 +666,11 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     cfg.gridDim = dim3(p.G, 1, 1);
     cfg.blockDim = dim3(kKv8Threads, 1, 1);
     cfg.dynamicSmemBytes = kKv8Smem;
-    const bool qlo = d.kv_dtype != LSA_BF16, plo = p.rows > 4;
-    cudaError_t e = qlo ? (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<true, true>, p, kt, err)
-                               : cudaLaunchKernelEx(&cfg, k_kv8_attn<true, false>, p, kt, err))
-                        : (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<false, true>, p, kt, err)
-                               : cudaLaunchKernelEx(&cfg, k_kv8_attn<false, false>, p, kt, err));
+    const bool wide = d.kv_dtype != LSA_BF16, plo = p.rows > 4;
+    cudaError_t e = wide ? (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<3, true>, p, kt, err)
+                                : cudaLaunchKernelEx(&cfg, k_kv8_attn<3, false>, p, kt, err))
+                         : (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<1, true>, p, kt, err)
+                                : cudaLaunchKernelEx(&cfg, k_kv8_attn<1, false>, p, kt, err));
     if (e != cudaSuccess || !kv8_splits(kt, runs_b, p.F, p.G)) return e;
     cfg.numAttrs = 1;  // the merge always follows the split kernel: overlap its launch
     cfg.gridDim = dim3(p.G, p.rows, 4);
@@ -619,9 +679,12 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     return cudaLaunchKernelEx(&cfg, k_kv8_attn_merge, p, kt);
 }
 
-// Whether the tokens of one head are few enough to be counted in 32 bits.
-bool kv8_attn_fits(const SeqTable& tab, int c_log2) {
-    return ((int64_t)tab.kept_off[tab.B] << c_log2) + (int64_t)tab.B * kKv8Tile < (1ll << 31);
+// Whether the kept tokens of one head and the rows of the cache are few enough for 32-bit counts
+// (2^31 rows of K8 are 256 GiB). A lane looks up to two batches past its warp's last tile.
+bool kv8_attn_fits(const SeqTable& tab, const Kv8Geom& g) {
+    const int64_t slack = ((int64_t)tab.B + 2 * kKv8Batch * kKv8Warps) * kKv8Tile;
+    return ((int64_t)tab.kept_off[tab.B] << g.c_log2) + slack < (1ll << 31) &&
+           ((int64_t)tab.chunk_off[tab.B] << (g.c_log2 + g.h_log2)) < (1ll << 31);
 }
 
 }  // namespace lsa
