@@ -27,11 +27,12 @@
 //    output carries, so that the products stay within f16's range whatever the scales are.
 //  * The tensor cores truncate when they accumulate: each tile's product starts from zero and is added
 //    to the running output in fp32, rounded to nearest, by the multiply-add that also rescales it.
-//  * A warp streams tiles of 32 tokens of one (sequence, K/V head) run through its own two-slot ring in
-//    shared memory, filled by asynchronous copies (no barrier between warps); K's half of a slot is
-//    refilled as soon as S is done, V's after the second product: 96 KB in flight per SM. What it has
-//    to know of a tile (chunk id, row, scales, how many tokens exist) its lanes work out side by side
-//    for 32 groups of 8 tokens ("octets") at a time.
+//  * A warp streams tiles of 32 tokens of one (sequence, K/V head) run through its own 4 KB of K and 4 KB
+//    of V in shared memory, filled by asynchronous copies (no barrier between warps). Each part is
+//    refilled for the next tile as soon as it is read: with 16 warps on an SM a warp's step takes longer
+//    than memory does, so one tile ahead is enough, and few registers (128) matter more. What a warp has
+//    to know of a tile (chunk id, row, scales, how many tokens exist) its lanes work out side by side for
+//    32 groups of 8 tokens ("octets") at a time.
 //  * The tiles of all runs form one list that is split evenly over the CTAs; a CTA joins its warps in
 //    shared memory, and a run that spans CTAs is joined by k_kv8_attn_merge. Runs that one CTA holds
 //    whole are written at once.
@@ -45,12 +46,14 @@ constexpr int kKv8Tile = 32;       // tokens per tile: 4 octets
 constexpr int kKv8Batch = 8;       // tiles whose 32 octets the lanes hold
 constexpr int kKv8MaxRows = 8;     // query heads per run
 constexpr float kKv8PShift = 14.f; // weights are at most 2^14
-constexpr int kKv8SlotBytes = 2 * kKv8Tile * kDh;  // K rows, then V rows
-constexpr int kKv8SlotV = kKv8Tile * kDh;
-constexpr int kKv8WarpBytes = 2 * kKv8SlotBytes;
-constexpr int kKv8JoinBytes = kKv8Warps * kKv8MaxRows * (kDh + 2) * 4;  // takes the rings' place
-constexpr int kKv8Smem = kKv8Warps * kKv8WarpBytes;
-static_assert(kKv8JoinBytes <= kKv8Smem, "the join's buffers lie in the rings");
+constexpr int kKv8SlotV = kKv8Tile * kDh;          // a warp's shared memory: K rows, V rows,
+constexpr int kKv8Meta = 2 * kKv8Tile * kDh;       // a batch's ks[32] and vs / vref [32]
+constexpr int kKv8WarpBytes = kKv8Meta + 2 * 32 * 4;
+constexpr int kKv8JoinBytes = kKv8Warps * kKv8MaxRows * (kDh + 2) * 4;  // takes the tiles' place
+constexpr int kKv8TilesBytes = kKv8Warps * kKv8WarpBytes;
+static_assert(kKv8JoinBytes <= kKv8TilesBytes, "the join's buffers lie where the tiles were");
+static_assert(kKv8Warps == 4, "each warp splits a quarter of q");
+__host__ __device__ constexpr int kv8_smem(int sets) { return kKv8TilesBytes + sets * 4 * 32 * 16; }
 
 // Prefix tables of one call: the kept (or all) chunks and their tiles.
 struct Kv8Tab {
@@ -82,19 +85,21 @@ __device__ __forceinline__ float kv8_ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
+// d = a b + c; c may be zeros, which cost no registers.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1, const float (&c)[4]) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
@@ -128,7 +133,7 @@ struct Kv8Octet {
 // grid G, kKv8Threads threads. SETS: products of S, two terms of q each (bf16: 1, fp32: 3); PLO: groups
 // of 8 (a second product for P's low halves).
 template <int SETS, bool PLO>
-__global__ void __launch_bounds__(kKv8Threads, SETS == 1 ? 3 : 2)  // what the rings leave room for, and q's terms
+__global__ void __launch_bounds__(kKv8Threads, 4)
 k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     extern __shared__ __align__(128) uint8_t smem[];
     float(*s_o)[kKv8MaxRows][kDh] = reinterpret_cast<float(*)[kKv8MaxRows][kDh]>(smem);
@@ -140,7 +145,8 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     const int my_row = g & (p.rows - 1);
     const int c_log2 = p.g.c_log2;
     const bool contig = c_log2 >= 5;  // a tile's octets follow one another in the cache
-    const uint32_t ring = smem_u32(smem) + warp * kKv8WarpBytes;
+    const uint32_t slot = smem_u32(smem) + warp * kKv8WarpBytes, meta = slot + kKv8Meta;
+    const uint32_t qs = smem_u32(smem) + kKv8TilesBytes + lane * 16;  // q's terms: [set][step][lane]
     // A row's 16-byte units are XOR-swizzled by the row: the copies' and both fragments' accesses are
     // free of bank conflicts. Offsets of this lane within an octet (8 rows, 1 KB):
     const uint32_t cp0 = (lane >> 3) * kDh + (((lane & 7) ^ (lane >> 3)) << 4);
@@ -214,12 +220,11 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             nz = __ballot_sync(0xffffffffu, oct.n > 0);
             fetch_id(i + kKv8Batch);
         };
-        // Copies of tile i's K or V rows into its slot, one group for each (empty past the end). Octets
-        // without tokens are not copied; of the others all 8 rows are (they lie in the cache).
-        auto copy = [&](int i, const uint8_t* base, uint32_t off) {
+        // Copies of tile i's K or V rows, one group for each (empty past the end). Octets without tokens
+        // are not copied; of the others all 8 rows are (they lie in the cache).
+        auto copy = [&](int i, const uint8_t* base, uint32_t dst) {
             if (i < n_it) {
                 const int l0 = 4 * (i & (kKv8Batch - 1));
-                const uint32_t dst = ring + (i & 1) * kKv8SlotBytes + off;
                 if (contig) {  // if the first octet has no tokens, the later ones have none either
                     const uint32_t row = __shfl_sync(0xffffffffu, oct.row, l0);
                     if (nz >> l0 & 1) {
@@ -247,14 +252,11 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
 
         fetch_id(0);
         next_batch(0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            copy(i, p.K8, 0);
-            copy(i, p.V8, kKv8SlotV);
-        }
+        copy(0, p.K8, slot);
+        copy(0, p.V8, slot + kKv8SlotV);
 
-        // ---- q: 32 values of row my_row, scaled to stay below 256, as e4m3 terms worth 16^-i
-        uint32_t qa[SETS][4][4];
+        // ---- q: row my_row, scaled to stay below 256, as e4m3 terms worth 16^-i; each warp does a step's
+        // share of the 128 values (8 per lane)
         float qmul;
         {
             const int64_t at = (int64_t)(qrow0 + my_row) * kDh + t * 32;
@@ -284,41 +286,44 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             // a row with an infinity or a NaN has no finite scores
             const uint32_t bad = __ballot_sync(0xffffffffu, nan || !(top < INFINITY));
             if (bad >> (lane & 28) & 15) qmul = __uint_as_float(0x7fc00000u);
+            float y[8];
+            load(warp, y);
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                float y[8];
-                load(s, y);
+            for (int e = 0; e < 8; ++e) y[e] *= up;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] *= up;
+            for (int k = 0; k < SETS; ++k) {
+                uint32_t a[4];  // the 16-row operand's registers: term 2 k in rows 0..7, 2 k + 1 in rows 8..15
 #pragma unroll
-                for (int k = 0; k < 2 * SETS; ++k) {
+                for (int j = 0; j < 2; ++j) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t w = e4m3x4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-                        qa[k >> 1][s][2 * i + (k & 1)] = w;
+                        a[2 * i + j] = w;
                         float f[4];
                         e4m3x4_floats(w, f);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[4 * i + e] = (y[4 * i + e] - f[e]) * 16.f;
                     }
                 }
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (k * 4 + warp) * 512), "r"(a[0]),
+                             "r"(a[1]), "r"(a[2]), "r"(a[3])
+                             : "memory");
             }
         }
+        __syncthreads();
 
         float o[8][4], m = -INFINITY, l = 0.f, vref = 0.f;
-        float rv = 0.f, ks = 0.f;  // this lane's octet of the batch being read: vs / vref and ks
-        uint32_t full = 0;         // octets whose 8 tokens all take part
-        int n = 0;
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t full = 0;  // octets of the batch in use whose 8 tokens all take part
+        int n = 0;          // tokens of this lane's octet of that batch
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
         for (int it = 0; it < n_it; ++it) {
-            const uint32_t slot = ring + (it & 1) * kKv8SlotBytes;
             const int l0 = 4 * (it & (kKv8Batch - 1));
             float vf = 1.f;
-            if (l0 == 0) {  // a new batch: its scales, and V's reference
+            if (l0 == 0) {  // a new batch: its scales, and V's reference, which it may raise
                 n = oct.n;
-                ks = oct.ks;
                 full = __ballot_sync(0xffffffffu, n == 8);
                 float vtop = oct.vs;
 #pragma unroll
@@ -327,30 +332,54 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                     vf = vref / vtop;
                     vref = vtop;
                 }
-                rv = vref > 0.f ? oct.vs / vref : 0.f;
+                const float rv = vref > 0.f ? oct.vs / vref : 0.f;
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(meta + 4 * lane), "f"(oct.ks) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(meta + 128 + 4 * lane), "f"(rv) : "memory");
             }
             const bool whole = (full >> l0 & 15u) == 15u;
 
             // ---- S: the terms of q against the tile's tokens
-            cp_async_wait<3>();
-            __syncwarp();  // every lane's copies of these rows have landed
+            cp_async_wait<1>();
+            __syncwarp();  // every lane's copies of K have landed
             float sc[8];
+            {
+                const uint4 k4 = kv8_lds16(meta + 4 * l0);
+                const float ks[4] = {__uint_as_float(k4.x), __uint_as_float(k4.y), __uint_as_float(k4.z),
+                                     __uint_as_float(k4.w)};
+                uint32_t kw[4][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 ka = kv8_lds16(slot + k_at0 + i * 8 * kDh), kb = kv8_lds16(slot + k_at1 + i * 8 * kDh);
-                const uint32_t kw[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
-                float s0 = 0.f, s1 = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 ka = kv8_lds16(slot + k_at0 + i * 8 * kDh), kb = kv8_lds16(slot + k_at1 + i * 8 * kDh);
+                    kw[i][0] = ka.x; kw[i][1] = ka.y; kw[i][2] = ka.z; kw[i][3] = ka.w;
+                    kw[i][4] = kb.x; kw[i][5] = kb.y; kw[i][6] = kb.z; kw[i][7] = kb.w;
+                }
 #pragma unroll
                 for (int k = SETS - 1; k >= 0; --k) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    float c[4][4];
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) mma_e4m3(c, qa[k][s], kw[2 * s], kw[2 * s + 1]);
-                    s0 = fmaf(fmaf(s0, 0.0625f, c[2]), 0.0625f, c[0]);
-                    s1 = fmaf(fmaf(s1, 0.0625f, c[3]), 0.0625f, c[1]);
+                    for (int s = 0; s < 4; ++s) {
+                        const uint4 a = kv8_lds16(qs + (k * 4 + s) * 512);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (s == 0) mma_e4m3(c[i], a, kw[i][0], kw[i][1], zero);
+                            else mma_e4m3(c[i], a, kw[i][2 * s], kw[i][2 * s + 1], c[i]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float hi = k == SETS - 1 ? c[i][2 + e] : fmaf(sc[2 * i + e], 0.0625f, c[i][2 + e]);
+                            sc[2 * i + e] = fmaf(hi, 0.0625f, c[i][e]);
+                        }
+                    }
                 }
-                const float f = qmul * __shfl_sync(0xffffffffu, ks, l0 + i);
-                sc[2 * i] = s0 * f;
-                sc[2 * i + 1] = s1 * f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = qmul * ks[i];
+                    sc[2 * i] *= f;
+                    sc[2 * i + 1] *= f;
+                }
             }
             if (!whole) {
 #pragma unroll
@@ -360,9 +389,9 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                     if (2 * t + 1 >= ni) sc[2 * i + 1] = -INFINITY;
                 }
             }
-            __syncwarp();  // the slot's K rows are read
-            if ((it + 2) % kKv8Batch == 0) next_batch(it + 2);
-            copy(it + 2, p.K8, 0);
+            __syncwarp();  // the K rows are read
+            if ((it + 1) % kKv8Batch == 0) next_batch(it + 1);
+            copy(it + 1, p.K8, slot);
 
             // ---- running maximum of row my_row
             float mx = m;
@@ -378,23 +407,28 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             // ---- weights (times 2^14, which out = O / l cancels) and their f16 halves
             const float ms = ref - kKv8PShift;
             uint32_t ph[4], pl[PLO ? 4 : 1];
-            l *= al;
+            {
+                const uint4 r4 = kv8_lds16(meta + 128 + 4 * l0);
+                const float rv[4] = {__uint_as_float(r4.x), __uint_as_float(r4.y), __uint_as_float(r4.z),
+                                     __uint_as_float(r4.w)};
+                float ls = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p0 = kv8_ex2(sc[2 * i] - ms), p1 = kv8_ex2(sc[2 * i + 1] - ms);
-                l += p0 + p1;
-                const float r = __shfl_sync(0xffffffffu, rv, l0 + i);
-                const float w0 = p0 * r, w1 = p1 * r;
-                ph[i] = f16x2_rn(w0, w1);
-                const float2 f = f16x2_floats(ph[i]);
-                const uint32_t low = f16x2_rn(w0 - f.x, w1 - f.y);
-                if constexpr (PLO) pl[i] = low;
-                else if (g >= 4) ph[i] = low;  // columns 4..7 carry the low halves of columns 0..3
+                for (int i = 0; i < 4; ++i) {
+                    const float p0 = kv8_ex2(sc[2 * i] - ms), p1 = kv8_ex2(sc[2 * i + 1] - ms);
+                    ls += p0 + p1;
+                    const float w0 = p0 * rv[i], w1 = p1 * rv[i];
+                    ph[i] = f16x2_rn(w0, w1);
+                    const float2 f = f16x2_floats(ph[i]);
+                    const uint32_t low = f16x2_rn(w0 - f.x, w1 - f.y);
+                    if constexpr (PLO) pl[i] = low;
+                    else ph[i] = g >= 4 ? low : ph[i];  // columns 4..7 carry the low halves of columns 0..3
+                }
+                l = fmaf(l, al, ls);
             }
 
             // ---- O^T = O^T alpha + V^T P^T
-            cp_async_wait<3>();
-            __syncwarp();
+            cp_async_wait<1>();
+            __syncwarp();  // every lane's copies of V have landed
             uint4 vv[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -409,21 +443,22 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                     if (2 * t + 1 >= ni) vv[2 * i + 1] = make_uint4(0, 0, 0, 0);
                 }
             }
-            __syncwarp();  // the slot's V rows are read
-            copy(it + 2, p.V8, kKv8SlotV);
+            __syncwarp();  // the V rows are read
+            copy(it + 1, p.V8, slot + kKv8SlotV);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    float c[4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {  // tokens 0..15, 16..31 of the tile
                         const uint32_t y0 = __byte_perm((&vv[4 * e].x)[w], (&vv[4 * e + 1].x)[w], i ? 0x7362 : 0x5140);
                         const uint32_t y1 = __byte_perm((&vv[4 * e + 2].x)[w], (&vv[4 * e + 3].x)[w], i ? 0x7362 : 0x5140);
                         const uint32_t b0 = e4m3lo_f16x2(y0), b1 = e4m3hi_f16x2(y0);
                         const uint32_t b2 = e4m3lo_f16x2(y1), b3 = e4m3hi_f16x2(y1);
-                        mma_f16(c, b0, b1, b2, b3, ph[2 * e], ph[2 * e + 1]);
-                        if constexpr (PLO) mma_f16(c, b0, b1, b2, b3, pl[2 * e], pl[2 * e + 1]);
+                        if (e == 0) mma_f16(c, b0, b1, b2, b3, ph[0], ph[1], zero);
+                        else mma_f16(c, b0, b1, b2, b3, ph[2], ph[3], c);
+                        if constexpr (PLO) mma_f16(c, b0, b1, b2, b3, pl[2 * e], pl[2 * e + 1], c);
                     }
                     float(&oo)[4] = o[2 * w + i];
                     oo[0] = fmaf(oo[0], a0, c[0]);
@@ -444,7 +479,7 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                 for (int e = 0; e < 4; ++e) o[j][e] += __shfl_xor_sync(0xffffffffu, o[j][e], 2);
         }
         cp_async_wait<0>();
-        __syncthreads();  // the rings are done with
+        __syncthreads();  // the tiles are done with
         if (t == 0 && g < p.rows) {
             s_ml[warp][g][0] = m == -INFINITY ? -INFINITY : m - kKv8PShift;
             s_ml[warp][g][1] = l;
@@ -492,85 +527,110 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     }
 }
 
-// Join of the runs that span CTAs. grid (G, rows, 4): CTA c takes the run that begins in range c and
-// reaches past it (there is at most one), one of its rows, and 32 of the Dh columns. Warp k takes the
-// spanned CTAs k, k + 8, ...; a lane owns a column.
+// Join of the runs that span CTAs. grid (x, rows / row_loop, 4 / dim_loop) with x either the runs
+// (by_cta = 0) or, where there are more runs than CTAs, the CTAs: CTA c then takes the run that begins in
+// its range and reaches past it (there is at most one). A block joins one row and 32 of the Dh columns at
+// a time: warp k takes the spanned CTAs k, k + 8, ...; a lane owns a column.
 constexpr int kKv8MergeThreads = 256;
 constexpr int kKv8MergeWarps = kKv8MergeThreads / 32;
 constexpr int kKv8MergeU = 8;  // partials in flight per lane
+constexpr int kKv8MergeBlocks = 1200;
 
 __device__ __forceinline__ int kv8_cta_of(int64_t u, int64_t F, int G) { return (int)(((u + 1) * G + F - 1) / F - 1); }
 
 __global__ void __launch_bounds__(kKv8MergeThreads)
-k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab) {
+k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int by_cta, int row_loop, int dim_loop) {
     __shared__ float s_m[kKv8MergeWarps], s_l[kKv8MergeWarps], s_a[kKv8MergeWarps][32];
-    const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int runs_b = p.g.Hkv * p.rts;
-    const int64_t u0 = (int64_t)c * p.F / p.G, u1 = ((int64_t)c + 1) * p.F / p.G;
-    pdl_wait();
-    if (u1 == u0) return;
-    int lo = 0, hi = tab.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)tab.tile_off[mid] * runs_b <= u1 - 1) lo = mid; else hi = mid - 1;
+    int b, run, c;
+    int64_t r0, r1;  // the run's units
+    if (by_cta) {
+        c = blockIdx.x;
+        const int64_t u0 = (int64_t)c * p.F / p.G, u1 = ((int64_t)c + 1) * p.F / p.G;
+        int lo = 0, hi = tab.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)tab.tile_off[mid] * runs_b <= u1 - 1) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+        const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
+        const int64_t base = (int64_t)tab.tile_off[b] * runs_b;
+        run = (int)((u1 - 1 - base) / tiles);
+        r0 = base + (int64_t)run * tiles;
+        r1 = r0 + tiles;
+        if (u1 == u0 || r0 < u0 || r1 <= u1) return;
+    } else {
+        b = blockIdx.x / runs_b;
+        run = blockIdx.x - b * runs_b;
+        const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
+        r0 = (int64_t)tab.tile_off[b] * runs_b + (int64_t)run * tiles;
+        r1 = r0 + tiles;
+        c = kv8_cta_of(r0, p.F, p.G);
     }
-    const int b = lo, tiles = tab.tile_off[b + 1] - tab.tile_off[b];
-    const int64_t base = (int64_t)tab.tile_off[b] * runs_b;
-    const int run = (int)((u1 - 1 - base) / tiles);
-    const int64_t r0 = base + (int64_t)run * tiles, r1 = r0 + tiles;  // the run's units
-    if (r0 < u0 || r1 <= u1) return;
     const int ns = kv8_cta_of(r1 - 1, p.F, p.G) - c + 1;
-    const int d = blockIdx.z * 32 + lane;
+    if (ns == 1) return;  // written by the CTA that held it
+    const int first = r0 > (int64_t)c * p.F / p.G ? 1 : 0;
+    pdl_wait();
 
-    float m = -INFINITY, l = 0.f, a = 0.f;
-    for (int i0 = wp; i0 < ns; i0 += kKv8MergeWarps * kKv8MergeU) {
-        float v[kKv8MergeU], mu[kKv8MergeU], lu[kKv8MergeU];
+    for (int rd = 0; rd < row_loop * dim_loop; ++rd) {
+        const int row = blockIdx.y * row_loop + rd / dim_loop, d = (blockIdx.z * dim_loop + rd % dim_loop) * 32 + lane;
+        float m = -INFINITY, l = 0.f, a = 0.f;
+        for (int i0 = wp; i0 < ns; i0 += kKv8MergeWarps * kKv8MergeU) {
+            float v[kKv8MergeU], mu[kKv8MergeU], lu[kKv8MergeU];
 #pragma unroll
-        for (int k = 0; k < kKv8MergeU; ++k) {  // past the last: reload it with no weight
-            const int i = i0 + k * kKv8MergeWarps, ic = i < ns ? i : ns - 1;
-            const int64_t slot = 2 * (int64_t)(c + ic) + (ic == 0 && r0 > u0 ? 1 : 0);
-            v[k] = p.part_o[(slot * kKv8MaxRows + row) * kDh + d];
-            const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * kKv8MaxRows + row) * 2);
-            mu[k] = i < ns ? ml.x : -INFINITY;
-            lu[k] = ml.y;
-        }
-        float mc = m;
-#pragma unroll
-        for (int k = 0; k < kKv8MergeU; ++k) mc = fmaxf(mc, mu[k]);
-        if (mc == -INFINITY) continue;
-        const float f = m == -INFINITY ? 0.f : kv8_ex2(m - mc);
-        l *= f;
-        a *= f;
-#pragma unroll
-        for (int k = 0; k < kKv8MergeU; ++k) {
-            const float w = mu[k] == -INFINITY ? 0.f : kv8_ex2(mu[k] - mc);
-            if (w > 0.f) {
-                l = fmaf(w, lu[k], l);
-                a = fmaf(w, v[k], a);
+            for (int k = 0; k < kKv8MergeU; ++k) {
+                const int i = i0 + k * kKv8MergeWarps;
+                mu[k] = -INFINITY;
+                v[k] = lu[k] = 0.f;
+                if (i < ns) {
+                    const int64_t slot = 2 * (int64_t)(c + i) + (i == 0 ? first : 0);
+                    v[k] = p.part_o[(slot * kKv8MaxRows + row) * kDh + d];
+                    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * kKv8MaxRows + row) * 2);
+                    mu[k] = ml.x;
+                    lu[k] = ml.y;
+                }
             }
+            float mc = m;
+#pragma unroll
+            for (int k = 0; k < kKv8MergeU; ++k) mc = fmaxf(mc, mu[k]);
+            if (mc == -INFINITY) continue;
+            const float f = m == -INFINITY ? 0.f : kv8_ex2(m - mc);
+            l *= f;
+            a *= f;
+#pragma unroll
+            for (int k = 0; k < kKv8MergeU; ++k) {
+                if (mu[k] != -INFINITY) {
+                    const float w = kv8_ex2(mu[k] - mc);
+                    l = fmaf(w, lu[k], l);
+                    a = fmaf(w, v[k], a);
+                }
+            }
+            m = mc;
         }
-        m = mc;
-    }
-    if (lane == 0) {
-        s_m[wp] = m;
-        s_l[wp] = l;
-    }
-    s_a[wp][lane] = a;
-    __syncthreads();
-    if (wp != 0) return;
-    float M = -INFINITY, A = 0.f, L = 0.f;
+        if (lane == 0) {
+            s_m[wp] = m;
+            s_l[wp] = l;
+        }
+        s_a[wp][lane] = a;
+        __syncthreads();
+        if (wp == 0) {
+            float M = -INFINITY, A = 0.f, L = 0.f;
 #pragma unroll
-    for (int k = 0; k < kKv8MergeWarps; ++k) M = fmaxf(M, s_m[k]);
+            for (int k = 0; k < kKv8MergeWarps; ++k) M = fmaxf(M, s_m[k]);
 #pragma unroll
-    for (int k = 0; k < kKv8MergeWarps; ++k) {
-        const float w = s_m[k] == -INFINITY ? 0.f : kv8_ex2(s_m[k] - M);
-        A = fmaf(w, s_a[k][lane], A);
-        L = fmaf(w, s_l[k], L);
+            for (int k = 0; k < kKv8MergeWarps; ++k) {
+                const float w = s_m[k] == -INFINITY ? 0.f : kv8_ex2(s_m[k] - M);
+                A = fmaf(w, s_a[k][lane], A);
+                L = fmaf(w, s_l[k], L);
+            }
+            const int h = run / p.rts, rt = run - h * p.rts;
+            const int q = b * p.H + (h * p.rts + rt) * p.rows + row;
+            p.out[(int64_t)q * kDh + d] = L == 0.f ? 0.f : A / L;
+            if (d == 0 && p.lse != nullptr) p.lse[q] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        }
+        __syncthreads();
     }
-    const int h = run / p.rts, rt = run - h * p.rts;
-    const int q = b * p.H + (h * p.rts + rt) * p.rows + row;
-    p.out[(int64_t)q * kDh + d] = L == 0.f ? 0.f : A / L;
-    if (d == 0 && p.lse != nullptr) p.lse[q] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 // ------------------------------------------------------------------ host side
@@ -580,13 +640,14 @@ cudaError_t kv8_init_attrs(int num_sms, int* ctas) {
                                  {(const void*)k_kv8_attn<1, false>, (const void*)k_kv8_attn<1, true>}};
     for (int dt = 0; dt < 2; ++dt) {
         int occ = 0;
+        const int smem = kv8_smem(dt == LSA_BF16 ? 1 : 3);
         for (const void* k : kernels[dt]) {
             int n = 0;
-            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kKv8Smem);
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
                                          (int)cudaSharedmemCarveoutMaxShared);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kKv8Threads, kKv8Smem);
+            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kKv8Threads, smem);
             if (e != cudaSuccess) return e;
             if (occ == 0 || n < occ) occ = n;
         }
@@ -665,18 +726,24 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     cfg.numAttrs = pdl ? 1 : 0;
     cfg.gridDim = dim3(p.G, 1, 1);
     cfg.blockDim = dim3(kKv8Threads, 1, 1);
-    cfg.dynamicSmemBytes = kKv8Smem;
     const bool wide = d.kv_dtype != LSA_BF16, plo = p.rows > 4;
+    cfg.dynamicSmemBytes = kv8_smem(wide ? 3 : 1);
     cudaError_t e = wide ? (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<3, true>, p, kt, err)
                                 : cudaLaunchKernelEx(&cfg, k_kv8_attn<3, false>, p, kt, err))
                          : (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<1, true>, p, kt, err)
                                 : cudaLaunchKernelEx(&cfg, k_kv8_attn<1, false>, p, kt, err));
     if (e != cudaSuccess || !kv8_splits(kt, runs_b, p.F, p.G)) return e;
     cfg.numAttrs = 1;  // the merge always follows the split kernel: overlap its launch
-    cfg.gridDim = dim3(p.G, p.rows, 4);
+    // a block per row and 32 columns while that makes few blocks (about four an SM), else blocks that loop
+    const int by_cta = runs > p.G ? 1 : 0;
+    const int64_t x = by_cta ? p.G : runs;
+    int ny = p.rows, nz = 4;
+    while (nz > 1 && x * ny * nz > kKv8MergeBlocks) nz >>= 1;
+    while (ny > 1 && x * ny * nz > kKv8MergeBlocks) ny >>= 1;
+    cfg.gridDim = dim3((unsigned)x, ny, nz);
     cfg.blockDim = dim3(kKv8MergeThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, k_kv8_attn_merge, p, kt);
+    return cudaLaunchKernelEx(&cfg, k_kv8_attn_merge, p, kt, by_cta, p.rows / ny, 4 / nz);
 }
 
 // Whether the kept tokens of one head and the rows of the cache are few enough for 32-bit counts
