@@ -122,6 +122,27 @@ __device__ __forceinline__ uint4 kv8_lds16(uint32_t addr) {
     return v;
 }
 
+// a / b for 0 <= a, 0 < b: in 32 bits where both fit, which is nearly always.
+__device__ __forceinline__ int64_t kv8_div(int64_t a, int64_t b) {
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// The CTA whose range [c F / G, (c + 1) F / G) holds unit u.
+__device__ __forceinline__ int kv8_cta_of(int64_t u, int64_t F, int G) {
+    return (int)(kv8_div((u + 1) * G + F - 1, F) - 1);
+}
+
+// The sequence whose runs hold unit u.
+__device__ __forceinline__ int kv8_seq_of(const Kv8Tab& tab, int runs_b, int64_t u) {
+    int lo = 0, hi = tab.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)tab.tile_off[mid] * runs_b <= u) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
 // One lane's octet of a batch: its first row in the cache (in rows of Dh bytes), how many of its 8
 // tokens take part, its scales.
 struct Kv8Octet {
@@ -140,7 +161,7 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     float(*s_ml)[kKv8MaxRows][2] =
         reinterpret_cast<float(*)[kKv8MaxRows][2]>(smem + kKv8Warps * kKv8MaxRows * kDh * 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int64_t u0 = (int64_t)blockIdx.x * p.F / p.G, u1 = ((int64_t)blockIdx.x + 1) * p.F / p.G;
+    const int64_t u0 = kv8_div((int64_t)blockIdx.x * p.F, p.G), u1 = kv8_div(((int64_t)blockIdx.x + 1) * p.F, p.G);
     const int runs_b = p.g.Hkv * p.rts;
     const int my_row = g & (p.rows - 1);
     const int c_log2 = p.g.c_log2;
@@ -157,21 +178,13 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     pdl_trigger();
     pdl_wait();
 
-    int b = 0;
-    {
-        int lo = 0, hi = tab.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)tab.tile_off[mid] * runs_b <= u0) lo = mid; else hi = mid - 1;
-        }
-        b = lo;
-    }
+    int b = kv8_seq_of(tab, runs_b, u0);
     for (int64_t u = u0; u < u1;) {
         // ---- the run that holds unit u
         while (u >= (int64_t)tab.tile_off[b + 1] * runs_b) ++b;
         const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
         const int64_t rel = u - (int64_t)tab.tile_off[b] * runs_b;
-        const int run = (int)(rel / tiles);
+        const int run = (int)kv8_div(rel, tiles);
         const int tile0 = (int)(rel - (int64_t)run * tiles);
         const int tile1 = (int)min((int64_t)tiles, tile0 + (u1 - u));
         const int h = run / p.rts, rt = run - h * p.rts;
@@ -527,109 +540,114 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     }
 }
 
-// Join of the runs that span CTAs. grid (x, rows / row_loop, 4 / dim_loop) with x either the runs
-// (by_cta = 0) or, where there are more runs than CTAs, the CTAs: CTA c then takes the run that begins in
-// its range and reaches past it (there is at most one). A block joins one row and 32 of the Dh columns at
-// a time: warp k takes the spanned CTAs k, k + 8, ...; a lane owns a column.
-constexpr int kKv8MergeThreads = 256;
-constexpr int kKv8MergeWarps = kKv8MergeThreads / 32;
+// Join of the runs that span CTAs: `wpr` warps to a row, a lane owns four of its Dh columns. The rows are
+// those of all runs (by_cta = 0) or, where there are more runs than CTAs, of the CTAs: CTA c then stands
+// for the run that begins in its range and reaches past it (there is at most one).
 constexpr int kKv8MergeU = 8;  // partials in flight per lane
-constexpr int kKv8MergeBlocks = 1200;
 
-__device__ __forceinline__ int kv8_cta_of(int64_t u, int64_t F, int G) { return (int)(((u + 1) * G + F - 1) / F - 1); }
-
-__global__ void __launch_bounds__(kKv8MergeThreads)
-k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int by_cta, int row_loop, int dim_loop) {
-    __shared__ float s_m[kKv8MergeWarps], s_l[kKv8MergeWarps], s_a[kKv8MergeWarps][32];
+__global__ void __launch_bounds__(1024)
+k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int by_cta, int wpr, int64_t n_rows) {
+    extern __shared__ __align__(16) float s_join[];  // [warp][Dh + 4]: columns, m, l
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int runs_b = p.g.Hkv * p.rts;
-    int b, run, c;
-    int64_t r0, r1;  // the run's units
-    if (by_cta) {
-        c = blockIdx.x;
-        const int64_t u0 = (int64_t)c * p.F / p.G, u1 = ((int64_t)c + 1) * p.F / p.G;
-        int lo = 0, hi = tab.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)tab.tile_off[mid] * runs_b <= u1 - 1) lo = mid; else hi = mid - 1;
+    const int64_t r = ((int64_t)blockIdx.x * (blockDim.x >> 5) + wp) / wpr;
+    const int sub = wp & (wpr - 1);
+    const int row = (int)(r & (p.rows - 1));
+    int b = 0, run = 0, c = 0, ns = 0, first = 0;
+    if (r < n_rows) {
+        const int64_t x = r / p.rows;  // run or CTA
+        int64_t r0, r1;                // the run's units
+        bool mine = true;
+        if (by_cta) {
+            c = (int)x;
+            const int64_t u0 = kv8_div((int64_t)c * p.F, p.G), u1 = kv8_div(((int64_t)c + 1) * p.F, p.G);
+            b = kv8_seq_of(tab, runs_b, u1 - 1);
+            const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
+            const int64_t base = (int64_t)tab.tile_off[b] * runs_b;
+            run = (int)kv8_div(u1 - 1 - base, tiles);
+            r0 = base + (int64_t)run * tiles;
+            r1 = r0 + tiles;
+            mine = u1 > u0 && r0 >= u0 && r1 > u1;
+        } else {
+            b = (int)x / runs_b;
+            run = (int)x - b * runs_b;
+            const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
+            r0 = (int64_t)tab.tile_off[b] * runs_b + (int64_t)run * tiles;
+            r1 = r0 + tiles;
+            c = kv8_cta_of(r0, p.F, p.G);
         }
-        b = lo;
-        const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
-        const int64_t base = (int64_t)tab.tile_off[b] * runs_b;
-        run = (int)((u1 - 1 - base) / tiles);
-        r0 = base + (int64_t)run * tiles;
-        r1 = r0 + tiles;
-        if (u1 == u0 || r0 < u0 || r1 <= u1) return;
-    } else {
-        b = blockIdx.x / runs_b;
-        run = blockIdx.x - b * runs_b;
-        const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
-        r0 = (int64_t)tab.tile_off[b] * runs_b + (int64_t)run * tiles;
-        r1 = r0 + tiles;
-        c = kv8_cta_of(r0, p.F, p.G);
+        if (mine) {
+            ns = kv8_cta_of(r1 - 1, p.F, p.G) - c + 1;
+            first = r0 > kv8_div((int64_t)c * p.F, p.G) ? 1 : 0;
+        }
     }
-    const int ns = kv8_cta_of(r1 - 1, p.F, p.G) - c + 1;
-    if (ns == 1) return;  // written by the CTA that held it
-    const int first = r0 > (int64_t)c * p.F / p.G ? 1 : 0;
     pdl_wait();
-
-    for (int rd = 0; rd < row_loop * dim_loop; ++rd) {
-        const int row = blockIdx.y * row_loop + rd / dim_loop, d = (blockIdx.z * dim_loop + rd % dim_loop) * 32 + lane;
-        float m = -INFINITY, l = 0.f, a = 0.f;
-        for (int i0 = wp; i0 < ns; i0 += kKv8MergeWarps * kKv8MergeU) {
-            float v[kKv8MergeU], mu[kKv8MergeU], lu[kKv8MergeU];
+    // ns == 1: written by the CTA that held the run
+    float m = -INFINITY, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ns > 1) {
+        for (int i0 = sub; i0 < ns; i0 += wpr * kKv8MergeU) {
+            float4 v[kKv8MergeU];
+            float2 ml[kKv8MergeU];
 #pragma unroll
             for (int k = 0; k < kKv8MergeU; ++k) {
-                const int i = i0 + k * kKv8MergeWarps;
-                mu[k] = -INFINITY;
-                v[k] = lu[k] = 0.f;
+                const int i = i0 + k * wpr;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                ml[k] = make_float2(-INFINITY, 0.f);
                 if (i < ns) {
-                    const int64_t slot = 2 * (int64_t)(c + i) + (i == 0 ? first : 0);
-                    v[k] = p.part_o[(slot * kKv8MaxRows + row) * kDh + d];
-                    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * kKv8MaxRows + row) * 2);
-                    mu[k] = ml.x;
-                    lu[k] = ml.y;
+                    const int64_t at = (2 * (int64_t)(c + i) + (i == 0 ? first : 0)) * kKv8MaxRows + row;
+                    v[k] = *reinterpret_cast<const float4*>(p.part_o + at * kDh + lane * 4);
+                    ml[k] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
                 }
             }
             float mc = m;
 #pragma unroll
-            for (int k = 0; k < kKv8MergeU; ++k) mc = fmaxf(mc, mu[k]);
+            for (int k = 0; k < kKv8MergeU; ++k) mc = fmaxf(mc, ml[k].x);
             if (mc == -INFINITY) continue;
             const float f = m == -INFINITY ? 0.f : kv8_ex2(m - mc);
             l *= f;
-            a *= f;
+            a.x *= f; a.y *= f; a.z *= f; a.w *= f;
 #pragma unroll
             for (int k = 0; k < kKv8MergeU; ++k) {
-                if (mu[k] != -INFINITY) {
-                    const float w = kv8_ex2(mu[k] - mc);
-                    l = fmaf(w, lu[k], l);
-                    a = fmaf(w, v[k], a);
+                if (ml[k].x != -INFINITY) {
+                    const float w = kv8_ex2(ml[k].x - mc);
+                    l = fmaf(w, ml[k].y, l);
+                    a.x = fmaf(w, v[k].x, a.x); a.y = fmaf(w, v[k].y, a.y);
+                    a.z = fmaf(w, v[k].z, a.z); a.w = fmaf(w, v[k].w, a.w);
                 }
             }
             m = mc;
         }
+    }
+    if (wpr > 1) {
+        float* mine = s_join + wp * (kDh + 4);
+        *reinterpret_cast<float4*>(mine + lane * 4) = a;
         if (lane == 0) {
-            s_m[wp] = m;
-            s_l[wp] = l;
-        }
-        s_a[wp][lane] = a;
-        __syncthreads();
-        if (wp == 0) {
-            float M = -INFINITY, A = 0.f, L = 0.f;
-#pragma unroll
-            for (int k = 0; k < kKv8MergeWarps; ++k) M = fmaxf(M, s_m[k]);
-#pragma unroll
-            for (int k = 0; k < kKv8MergeWarps; ++k) {
-                const float w = s_m[k] == -INFINITY ? 0.f : kv8_ex2(s_m[k] - M);
-                A = fmaf(w, s_a[k][lane], A);
-                L = fmaf(w, s_l[k], L);
-            }
-            const int h = run / p.rts, rt = run - h * p.rts;
-            const int q = b * p.H + (h * p.rts + rt) * p.rows + row;
-            p.out[(int64_t)q * kDh + d] = L == 0.f ? 0.f : A / L;
-            if (d == 0 && p.lse != nullptr) p.lse[q] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+            mine[kDh] = m;
+            mine[kDh + 1] = l;
         }
         __syncthreads();
+        if (sub != 0) return;
+        m = -INFINITY;
+        l = 0.f;
+        a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < wpr; ++k) m = fmaxf(m, mine[k * (kDh + 4) + kDh]);
+        for (int k = 0; k < wpr; ++k) {
+            const float* o = mine + k * (kDh + 4);
+            if (o[kDh] == -INFINITY) continue;
+            const float w = kv8_ex2(o[kDh] - m);
+            const float4 v = *reinterpret_cast<const float4*>(o + lane * 4);
+            l = fmaf(w, o[kDh + 1], l);
+            a.x = fmaf(w, v.x, a.x); a.y = fmaf(w, v.y, a.y);
+            a.z = fmaf(w, v.z, a.z); a.w = fmaf(w, v.w, a.w);
+        }
+    }
+    if (ns > 1) {
+        const int h = run / p.rts, rt = run - h * p.rts;
+        const int q = b * p.H + (h * p.rts + rt) * p.rows + row;
+        const float4 y = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x / l, a.y / l, a.z / l, a.w / l);
+        *reinterpret_cast<float4*>(p.out + (int64_t)q * kDh + lane * 4) = y;
+        if (lane == 0 && p.lse != nullptr) p.lse[q] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
 }
 
@@ -734,16 +752,16 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
                                 : cudaLaunchKernelEx(&cfg, k_kv8_attn<1, false>, p, kt, err));
     if (e != cudaSuccess || !kv8_splits(kt, runs_b, p.F, p.G)) return e;
     cfg.numAttrs = 1;  // the merge always follows the split kernel: overlap its launch
-    // a block per row and 32 columns while that makes few blocks (about four an SM), else blocks that loop
+    // One warp to a row where a run spans few CTAs; eight, and 32 (a block), where it spans many.
     const int by_cta = runs > p.G ? 1 : 0;
-    const int64_t x = by_cta ? p.G : runs;
-    int ny = p.rows, nz = 4;
-    while (nz > 1 && x * ny * nz > kKv8MergeBlocks) nz >>= 1;
-    while (ny > 1 && x * ny * nz > kKv8MergeBlocks) ny >>= 1;
-    cfg.gridDim = dim3((unsigned)x, ny, nz);
-    cfg.blockDim = dim3(kKv8MergeThreads, 1, 1);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, k_kv8_attn_merge, p, kt, by_cta, p.rows / ny, 4 / nz);
+    const int64_t span = p.G / runs;
+    const int wpr = span <= 8 ? 1 : span <= 64 ? 8 : 32;
+    const int threads = wpr == 32 ? 1024 : 256;
+    const int64_t n_rows = (by_cta ? p.G : runs) * p.rows;
+    cfg.gridDim = dim3((unsigned)((n_rows * wpr * 32 + threads - 1) / threads), 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = wpr == 1 ? 0 : threads / 32 * (kDh + 4) * 4;
+    return cudaLaunchKernelEx(&cfg, k_kv8_attn_merge, p, kt, by_cta, wpr, n_rows);
 }
 
 // Whether the kept tokens of one head and the rows of the cache are few enough for 32-bit counts
