@@ -40,8 +40,10 @@
 
 namespace lsa {
 
-constexpr int kKv8Warps = 4;
-constexpr int kKv8Threads = kKv8Warps * 32;
+constexpr int kKv8Warps = 4;       // of a CTA; four CTAs to an SM
+constexpr int kKv8WideWarps = 16;  // of a CTA that holds a short run whole
+constexpr int kKv8WideTiles = 64;  // tiles of the longest run that such a CTA takes
+constexpr int kKv8RunCost = 8;     // what another run costs a CTA, in tiles
 constexpr int kKv8Tile = 32;       // tokens per tile: 4 octets
 constexpr int kKv8Batch = 8;       // tiles whose 32 octets the lanes hold
 constexpr int kKv8MaxRows = 8;     // query heads per run
@@ -49,18 +51,16 @@ constexpr float kKv8PShift = 14.f; // weights are at most 2^14
 constexpr int kKv8SlotV = kKv8Tile * kDh;          // a warp's shared memory: K rows, V rows,
 constexpr int kKv8Meta = 2 * kKv8Tile * kDh;       // a batch's ks[32] and vs / vref [32]
 constexpr int kKv8WarpBytes = kKv8Meta + 2 * 32 * 4;
-constexpr int kKv8JoinBytes = kKv8Warps * kKv8MaxRows * (kDh + 2) * 4;  // takes the tiles' place
-constexpr int kKv8TilesBytes = kKv8Warps * kKv8WarpBytes;
-static_assert(kKv8JoinBytes <= kKv8TilesBytes, "the join's buffers lie where the tiles were");
-static_assert(kKv8Warps == 4, "each warp splits a quarter of q");
-__host__ __device__ constexpr int kv8_smem(int sets) { return kKv8TilesBytes + sets * 4 * 32 * 16; }
+constexpr int kKv8JoinBytes = kKv8MaxRows * (kDh + 2) * 4;  // of a warp; takes the tiles' place
+static_assert(kKv8JoinBytes <= kKv8WarpBytes, "the join's buffers lie where the tiles were");
+__host__ __device__ constexpr int kv8_smem(int sets, int warps) { return warps * kKv8WarpBytes + sets * 4 * 32 * 16; }
 
 // Prefix tables of one call: the kept (or all) chunks and their tiles.
 struct Kv8Tab {
     int32_t B;
     int32_t chunk_off[kMaxB + 1];
     int32_t kept_off[kMaxB + 1];
-    int32_t tile_off[kMaxB + 1];  // prefix of the tiles of one (sequence, head) run
+    int32_t cost_off[kMaxB + 1];  // prefix of the cost of one (sequence, head) run: its tiles + kKv8RunCost
 };
 
 struct Kv8AttnParams {
@@ -74,7 +74,8 @@ struct Kv8AttnParams {
     int32_t rts;        // runs per K/V head: group / rows
     int32_t len_add;    // added to seq_len
     int32_t G;          // CTAs
-    int64_t F;          // tiles of all runs
+    int32_t by_run;     // a CTA takes one run whole, else an equal share of the cost
+    int64_t F;          // cost of all runs
     float qscale;       // log2(e) / sqrt(Dh)
 };
 
@@ -138,7 +139,7 @@ __device__ __forceinline__ int kv8_seq_of(const Kv8Tab& tab, int runs_b, int64_t
     int lo = 0, hi = tab.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)tab.tile_off[mid] * runs_b <= u) lo = mid; else hi = mid - 1;
+        if ((int64_t)tab.cost_off[mid] * runs_b <= u) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
@@ -151,23 +152,22 @@ struct Kv8Octet {
     float ks, vs;
 };
 
-// grid G, kKv8Threads threads. SETS: products of S, two terms of q each (bf16: 1, fp32: 3); PLO: groups
+// grid G, WARPS * 32 threads. SETS: products of S, two terms of q each (bf16: 1, fp32: 3); PLO: groups
 // of 8 (a second product for P's low halves).
-template <int SETS, bool PLO>
-__global__ void __launch_bounds__(kKv8Threads, 4)
+template <int SETS, bool PLO, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     extern __shared__ __align__(128) uint8_t smem[];
     float(*s_o)[kKv8MaxRows][kDh] = reinterpret_cast<float(*)[kKv8MaxRows][kDh]>(smem);
     float(*s_ml)[kKv8MaxRows][2] =
-        reinterpret_cast<float(*)[kKv8MaxRows][2]>(smem + kKv8Warps * kKv8MaxRows * kDh * 4);
+        reinterpret_cast<float(*)[kKv8MaxRows][2]>(smem + WARPS * kKv8MaxRows * kDh * 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int64_t u0 = kv8_div((int64_t)blockIdx.x * p.F, p.G), u1 = kv8_div(((int64_t)blockIdx.x + 1) * p.F, p.G);
     const int runs_b = p.g.Hkv * p.rts;
     const int my_row = g & (p.rows - 1);
     const int c_log2 = p.g.c_log2;
     const bool contig = c_log2 >= 5;  // a tile's octets follow one another in the cache
     const uint32_t slot = smem_u32(smem) + warp * kKv8WarpBytes, meta = slot + kKv8Meta;
-    const uint32_t qs = smem_u32(smem) + kKv8TilesBytes + lane * 16;  // q's terms: [set][step][lane]
+    const uint32_t qs = smem_u32(smem) + WARPS * kKv8WarpBytes + lane * 16;  // q's terms: [set][step][lane]
     // A row's 16-byte units are XOR-swizzled by the row: the copies' and both fragments' accesses are
     // free of bank conflicts. Offsets of this lane within an octet (8 rows, 1 KB):
     const uint32_t cp0 = (lane >> 3) * kDh + (((lane & 7) ^ (lane >> 3)) << 4);
@@ -178,15 +178,38 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     pdl_trigger();
     pdl_wait();
 
-    int b = kv8_seq_of(tab, runs_b, u0);
+    // This CTA's cost units. A run's first kKv8RunCost units are what beginning it costs; its tiles follow.
+    int b;
+    int64_t u0, u1;
+    if (p.by_run) {
+        b = blockIdx.x / runs_b;
+        const int cost = tab.cost_off[b + 1] - tab.cost_off[b];
+        u0 = (int64_t)tab.cost_off[b] * runs_b + (int64_t)(blockIdx.x - b * runs_b) * cost;
+        u1 = u0 + cost;
+    } else {
+        u0 = kv8_div((int64_t)blockIdx.x * p.F, p.G);
+        u1 = kv8_div(((int64_t)blockIdx.x + 1) * p.F, p.G);
+        b = kv8_seq_of(tab, runs_b, u0);
+    }
     for (int64_t u = u0; u < u1;) {
         // ---- the run that holds unit u
-        while (u >= (int64_t)tab.tile_off[b + 1] * runs_b) ++b;
-        const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
-        const int64_t rel = u - (int64_t)tab.tile_off[b] * runs_b;
-        const int run = (int)kv8_div(rel, tiles);
-        const int tile0 = (int)(rel - (int64_t)run * tiles);
-        const int tile1 = (int)min((int64_t)tiles, tile0 + (u1 - u));
+        while (u >= (int64_t)tab.cost_off[b + 1] * runs_b) ++b;
+        const int cost = tab.cost_off[b + 1] - tab.cost_off[b];
+        const int64_t rel = u - (int64_t)tab.cost_off[b] * runs_b;
+        const int run = (int)kv8_div(rel, cost);
+        const int from = (int)(rel - (int64_t)run * cost);
+        const int to = (int)min((int64_t)cost, from + (u1 - u));
+        const int tile0 = max(from - kKv8RunCost, 0), tile1 = max(to - kKv8RunCost, 0);
+        const bool all = from == 0 && to == cost;
+        const int64_t part = 2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1);  // where a part of a run is left
+        u += to - from;
+        if (!all && tile0 == tile1) {  // only of the beginning's cost
+            if (tid < p.rows) {
+                p.part_ml[(part * kKv8MaxRows + tid) * 2] = -INFINITY;
+                p.part_ml[(part * kKv8MaxRows + tid) * 2 + 1] = 0.f;
+            }
+            continue;
+        }
         const int h = run / p.rts, rt = run - h * p.rts;
         const int n_b = tab.chunk_off[b + 1] - tab.chunk_off[b];
         int kept = tab.kept_off[b + 1] - tab.kept_off[b];
@@ -196,16 +219,16 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         if (p.seq_len != nullptr) len = max((int64_t)0, min(len, (int64_t)p.seq_len[b] + p.len_add));
         if (ids == nullptr) kept = min(kept, (int)((len + (1 << c_log2) - 1) >> c_log2));
         const int qrow0 = b * p.H + (h * p.rts + rt) * p.rows;
-        // This warp's tiles are tile0 + warp + kKv8Warps * i, i < n_it, as far as there are tokens.
+        // This warp's tiles are tile0 + warp + WARPS * i, i < n_it, as far as there are tokens.
         const int last = min(tile1, (int)((((int64_t)kept << c_log2) + kKv8Tile - 1) / kKv8Tile));
-        const int n_it = (max(last - tile0 - warp, 0) + kKv8Warps - 1) / kKv8Warps;
+        const int n_it = (max(last - tile0 - warp, 0) + WARPS - 1) / WARPS;
 
         // ---- what the lanes know of the octets: lane L has octet L % 4 of tile (batch) + L / 4
         Kv8Octet oct = {0, 0, 0.f, 0.f};  // of the tiles being copied
         uint32_t nz = 0;                  // octets (lanes) with tokens
         int id_next = 0;
         auto token_of = [&](int i) {      // first token of this lane's octet in the batch of tile i
-            return (tile0 + warp + kKv8Warps * (i + (lane >> 2))) * kKv8Tile + 8 * (lane & 3);
+            return (tile0 + warp + WARPS * (i + (lane >> 2))) * kKv8Tile + 8 * (lane & 3);
         };
         auto fetch_id = [&](int i) {
             const int j = token_of(i) >> c_log2;
@@ -268,8 +291,8 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         copy(0, p.K8, slot);
         copy(0, p.V8, slot + kKv8SlotV);
 
-        // ---- q: row my_row, scaled to stay below 256, as e4m3 terms worth 16^-i; each warp does a step's
-        // share of the 128 values (8 per lane)
+        // ---- q: row my_row, scaled to stay below 256, as e4m3 terms worth 16^-i; each of four warps
+        // does a step's share of the 128 values (8 per lane)
         float qmul;
         {
             const int64_t at = (int64_t)(qrow0 + my_row) * kDh + t * 32;
@@ -300,11 +323,11 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             const uint32_t bad = __ballot_sync(0xffffffffu, nan || !(top < INFINITY));
             if (bad >> (lane & 28) & 15) qmul = __uint_as_float(0x7fc00000u);
             float y[8];
-            load(warp, y);
+            load(warp & 3, y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] *= up;
 #pragma unroll
-            for (int k = 0; k < SETS; ++k) {
+            for (int k = 0; k < SETS && warp < 4; ++k) {
                 uint32_t a[4];  // the 16-row operand's registers: term 2 k in rows 0..7, 2 k + 1 in rows 8..15
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -359,31 +382,37 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                 const uint4 k4 = kv8_lds16(meta + 4 * l0);
                 const float ks[4] = {__uint_as_float(k4.x), __uint_as_float(k4.y), __uint_as_float(k4.z),
                                      __uint_as_float(k4.w)};
-                uint32_t kw[4][8];
+                constexpr int OC = SETS == 1 ? 4 : 2;  // octets at a time: what the registers hold
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 ka = kv8_lds16(slot + k_at0 + i * 8 * kDh), kb = kv8_lds16(slot + k_at1 + i * 8 * kDh);
-                    kw[i][0] = ka.x; kw[i][1] = ka.y; kw[i][2] = ka.z; kw[i][3] = ka.w;
-                    kw[i][4] = kb.x; kw[i][5] = kb.y; kw[i][6] = kb.z; kw[i][7] = kb.w;
-                }
+                for (int i0 = 0; i0 < 4; i0 += OC) {
+                    uint32_t kw[OC][8];
 #pragma unroll
-                for (int k = SETS - 1; k >= 0; --k) {
-                    float c[4][4];
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const uint4 a = kv8_lds16(qs + (k * 4 + s) * 512);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (s == 0) mma_e4m3(c[i], a, kw[i][0], kw[i][1], zero);
-                            else mma_e4m3(c[i], a, kw[i][2 * s], kw[i][2 * s + 1], c[i]);
-                        }
+                    for (int i = 0; i < OC; ++i) {
+                        const uint4 ka = kv8_lds16(slot + k_at0 + (i0 + i) * 8 * kDh);
+                        const uint4 kb = kv8_lds16(slot + k_at1 + (i0 + i) * 8 * kDh);
+                        kw[i][0] = ka.x; kw[i][1] = ka.y; kw[i][2] = ka.z; kw[i][3] = ka.w;
+                        kw[i][4] = kb.x; kw[i][5] = kb.y; kw[i][6] = kb.z; kw[i][7] = kb.w;
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int k = SETS - 1; k >= 0; --k) {
+                        float c[OC][4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float hi = k == SETS - 1 ? c[i][2 + e] : fmaf(sc[2 * i + e], 0.0625f, c[i][2 + e]);
-                            sc[2 * i + e] = fmaf(hi, 0.0625f, c[i][e]);
+                        for (int s = 0; s < 4; ++s) {
+                            const uint4 a = kv8_lds16(qs + (k * 4 + s) * 512);
+#pragma unroll
+                            for (int i = 0; i < OC; ++i) {
+                                if (s == 0) mma_e4m3(c[i], a, kw[i][0], kw[i][1], zero);
+                                else mma_e4m3(c[i], a, kw[i][2 * s], kw[i][2 * s + 1], c[i]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < OC; ++i) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float& y = sc[2 * (i0 + i) + e];
+                                const float hi = k == SETS - 1 ? c[i][2 + e] : fmaf(y, 0.0625f, c[i][2 + e]);
+                                y = fmaf(hi, 0.0625f, c[i][e]);
+                            }
                         }
                     }
                 }
@@ -509,15 +538,13 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             }
         }
         __syncthreads();
-        const bool all = tile0 == 0 && tile1 == tiles;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1);
-        for (int i = tid; i < p.rows * kDh; i += kKv8Threads) {
+        for (int i = tid; i < p.rows * kDh; i += WARPS * 32) {
             const int row = i >> 7, d = i & (kDh - 1);
             float M = -INFINITY, A = 0.f, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kKv8Warps; ++w) M = fmaxf(M, s_ml[w][row][0]);
+            for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][row][0]);
 #pragma unroll
-            for (int w = 0; w < kKv8Warps; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 const float mw = s_ml[w][row][0];
                 const float f = mw == -INFINITY ? 0.f : kv8_ex2(mw - M);
                 A = fmaf(f, s_o[w][row][d], A);
@@ -528,15 +555,14 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                 if (d == 0 && p.lse != nullptr)
                     p.lse[qrow0 + row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
             } else {
-                p.part_o[(slot * kKv8MaxRows + row) * kDh + d] = A;
+                p.part_o[(part * kKv8MaxRows + row) * kDh + d] = A;
                 if (d == 0) {
-                    p.part_ml[(slot * kKv8MaxRows + row) * 2] = M;
-                    p.part_ml[(slot * kKv8MaxRows + row) * 2 + 1] = L;
+                    p.part_ml[(part * kKv8MaxRows + row) * 2] = M;
+                    p.part_ml[(part * kKv8MaxRows + row) * 2 + 1] = L;
                 }
             }
         }
         __syncthreads();  // the shared partials are free for the next run
-        u += tile1 - tile0;
     }
 }
 
@@ -562,18 +588,18 @@ k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int by_cta, int wpr, i
             c = (int)x;
             const int64_t u0 = kv8_div((int64_t)c * p.F, p.G), u1 = kv8_div(((int64_t)c + 1) * p.F, p.G);
             b = kv8_seq_of(tab, runs_b, u1 - 1);
-            const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
-            const int64_t base = (int64_t)tab.tile_off[b] * runs_b;
-            run = (int)kv8_div(u1 - 1 - base, tiles);
-            r0 = base + (int64_t)run * tiles;
-            r1 = r0 + tiles;
+            const int cost = tab.cost_off[b + 1] - tab.cost_off[b];
+            const int64_t base = (int64_t)tab.cost_off[b] * runs_b;
+            run = (int)kv8_div(u1 - 1 - base, cost);
+            r0 = base + (int64_t)run * cost;
+            r1 = r0 + cost;
             mine = u1 > u0 && r0 >= u0 && r1 > u1;
         } else {
             b = (int)x / runs_b;
             run = (int)x - b * runs_b;
-            const int tiles = tab.tile_off[b + 1] - tab.tile_off[b];
-            r0 = (int64_t)tab.tile_off[b] * runs_b + (int64_t)run * tiles;
-            r1 = r0 + tiles;
+            const int cost = tab.cost_off[b + 1] - tab.cost_off[b];
+            r0 = (int64_t)tab.cost_off[b] * runs_b + (int64_t)run * cost;
+            r1 = r0 + cost;
             c = kv8_cta_of(r0, p.F, p.G);
         }
         if (mine) {
@@ -652,26 +678,31 @@ k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int by_cta, int wpr, i
 }
 
 // ------------------------------------------------------------------ host side
-// CTAs that the device holds at once, per kv_dtype (LSA_F32, LSA_BF16); the kernels' attributes.
+template <int SETS, bool PLO, int WARPS>
+static cudaError_t kv8_set_attrs(int* least) {
+    const cudaError_t e = set_smem_attrs(k_kv8_attn<SETS, PLO, WARPS>, kv8_smem(SETS, WARPS));
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_kv8_attn<SETS, PLO, WARPS>, WARPS * 32,
+                                                                        kv8_smem(SETS, WARPS));
+    if (n < *least) *least = n;
+    return f;
+}
+
+// Kernel attributes; the CTAs (of kKv8Warps) that the device holds at once, whichever variant runs.
 cudaError_t kv8_init_attrs(int num_sms, int* ctas) {
-    const void* kernels[2][2] = {{(const void*)k_kv8_attn<3, false>, (const void*)k_kv8_attn<3, true>},
-                                 {(const void*)k_kv8_attn<1, false>, (const void*)k_kv8_attn<1, true>}};
-    for (int dt = 0; dt < 2; ++dt) {
-        int occ = 0;
-        const int smem = kv8_smem(dt == LSA_BF16 ? 1 : 3);
-        for (const void* k : kernels[dt]) {
-            int n = 0;
-            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         (int)cudaSharedmemCarveoutMaxShared);
-            if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, kKv8Threads, smem);
-            if (e != cudaSuccess) return e;
-            if (occ == 0 || n < occ) occ = n;
-        }
-        ctas[dt] = (occ < 1 ? 1 : occ) * num_sms;
-    }
-    return cudaSuccess;
+    int n = 16, wide = 16;
+    cudaError_t e = kv8_set_attrs<1, false, kKv8Warps>(&n);
+    if (e == cudaSuccess) e = kv8_set_attrs<1, true, kKv8Warps>(&n);
+    if (e == cudaSuccess) e = kv8_set_attrs<3, false, kKv8Warps>(&n);
+    if (e == cudaSuccess) e = kv8_set_attrs<3, true, kKv8Warps>(&n);
+    if (e == cudaSuccess) e = kv8_set_attrs<1, false, kKv8WideWarps>(&wide);
+    if (e == cudaSuccess) e = kv8_set_attrs<1, true, kKv8WideWarps>(&wide);
+    if (e == cudaSuccess) e = kv8_set_attrs<3, false, kKv8WideWarps>(&wide);
+    if (e == cudaSuccess) e = kv8_set_attrs<3, true, kKv8WideWarps>(&wide);
+    if (e == cudaSuccess && (n < 1 || wide < 1)) e = cudaErrorLaunchOutOfResources;
+    *ctas = n * num_sms;
+    return e;
 }
 
 size_t kv8_part_o_bytes(int ctas) { return (size_t)2 * ctas * kKv8MaxRows * kDh * 4; }
@@ -682,15 +713,28 @@ static bool kv8_splits(const Kv8Tab& tab, int runs_b, int64_t F, int G) {
     int b = 0;
     for (int c = 1; c < G; ++c) {
         const int64_t u = (int64_t)c * F / G;
-        while (u >= (int64_t)tab.tile_off[b + 1] * runs_b) ++b;
-        if ((u - (int64_t)tab.tile_off[b] * runs_b) % (tab.tile_off[b + 1] - tab.tile_off[b]) != 0) return true;
+        while (u >= (int64_t)tab.cost_off[b + 1] * runs_b) ++b;
+        if ((u - (int64_t)tab.cost_off[b] * runs_b) % (tab.cost_off[b + 1] - tab.cost_off[b]) != 0) return true;
     }
     return false;
 }
 
+template <int SETS>
+static cudaError_t kv8_launch(cudaLaunchConfig_t& cfg, const Kv8AttnParams& p, const Kv8Tab& kt, uint32_t* err) {
+    const int warps = p.by_run ? kKv8WideWarps : kKv8Warps;
+    const bool plo = p.rows > 4;
+    cfg.blockDim = dim3(warps * 32, 1, 1);
+    cfg.dynamicSmemBytes = kv8_smem(SETS, warps);
+    if (p.by_run)
+        return plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, true, kKv8WideWarps>, p, kt, err)
+                   : cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, false, kKv8WideWarps>, p, kt, err);
+    return plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, true, kKv8Warps>, p, kt, err)
+               : cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, false, kKv8Warps>, p, kt, err);
+}
+
 // `tab`: the kept chunks of each sequence, or all of them where ids is null.
 cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv8_cache& cache, const Kv8Geom& g,
-                            int max_ctas, const void* q, const int32_t* ids, const int32_t* counts,
+                            int num_sms, int max_ctas, const void* q, const int32_t* ids, const int32_t* counts,
                             const int32_t* seq_len, int len_add, float* part_o, float* part_ml, float* out,
                             float* lse, uint32_t* err, cudaStream_t stream, bool pdl) {
     Kv8AttnParams p = {};
@@ -716,23 +760,30 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
 
     Kv8Tab kt;
     kt.B = tab.B;
-    int64_t tiles = 0;
+    int64_t cost = 0;
+    int most = 0;  // tiles of the longest run
     for (int b = 0; b <= tab.B; ++b) {
         kt.chunk_off[b] = tab.chunk_off[b];
         kt.kept_off[b] = tab.kept_off[b];
-        kt.tile_off[b] = (int32_t)tiles;
-        if (b < tab.B)
-            tiles += (((int64_t)(tab.kept_off[b + 1] - tab.kept_off[b]) << g.c_log2) + kKv8Tile - 1) / kKv8Tile;
+        kt.cost_off[b] = (int32_t)cost;
+        if (b == tab.B) break;
+        const int64_t tokens = (int64_t)(tab.kept_off[b + 1] - tab.kept_off[b]) << g.c_log2;
+        const int tiles = (int)((tokens + kKv8Tile - 1) / kKv8Tile);
+        most = tiles > most ? tiles : most;
+        cost += tiles + kKv8RunCost;
     }
     const int runs_b = g.Hkv * p.rts;
     const int64_t runs = (int64_t)runs_b * tab.B;
-    p.F = tiles * runs_b;
-    // Few tiles: at least two to a warp, one CTA to a run if that is enough, so that nothing is left
-    // to join; many: every resident CTA an equal share.
-    int64_t G = (p.F + 2 * kKv8Warps - 1) / (2 * kKv8Warps);
-    if (G < runs) G = runs;
-    if (G > max_ctas) G = max_ctas;
-    if (G > p.F) G = p.F;
+    p.F = cost * runs_b;
+    // Short runs, few enough for one wide CTA an SM: a CTA to a run, and nothing is left to join. Else
+    // every resident CTA an equal share, but no less than a tile to a warp.
+    const bool by_run = runs <= num_sms && most <= kKv8WideTiles;
+    p.by_run = by_run;
+    int64_t G = runs;
+    if (!by_run) {
+        G = (p.F + kKv8Warps - 1) / kKv8Warps;
+        if (G > max_ctas) G = max_ctas;
+    }
     p.G = (int)G;
 
     cudaLaunchAttribute attr[1];
@@ -743,15 +794,10 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     cfg.gridDim = dim3(p.G, 1, 1);
-    cfg.blockDim = dim3(kKv8Threads, 1, 1);
-    const bool wide = d.kv_dtype != LSA_BF16, plo = p.rows > 4;
-    cfg.dynamicSmemBytes = kv8_smem(wide ? 3 : 1);
-    cudaError_t e = wide ? (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<3, true>, p, kt, err)
-                                : cudaLaunchKernelEx(&cfg, k_kv8_attn<3, false>, p, kt, err))
-                         : (plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<1, true>, p, kt, err)
-                                : cudaLaunchKernelEx(&cfg, k_kv8_attn<1, false>, p, kt, err));
-    if (e != cudaSuccess || !kv8_splits(kt, runs_b, p.F, p.G)) return e;
-    cfg.numAttrs = 1;  // the merge always follows the split kernel: overlap its launch
+    const int sets = d.kv_dtype == LSA_BF16 ? 1 : 3;
+    cudaError_t e = sets == 1 ? kv8_launch<1>(cfg, p, kt, err) : kv8_launch<3>(cfg, p, kt, err);
+    if (e != cudaSuccess || by_run || !kv8_splits(kt, runs_b, p.F, p.G)) return e;
+    cfg.numAttrs = 1;  // the join always follows the split kernel: overlap its launch
     // One warp to a row where a run spans few CTAs; eight, and 32 (a block), where it spans many.
     const int by_cta = runs > p.G ? 1 : 0;
     const int64_t span = p.G / runs;
@@ -767,7 +813,7 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
 // Whether the kept tokens of one head and the rows of the cache are few enough for 32-bit counts
 // (2^31 rows of K8 are 256 GiB). A lane looks up to two batches past its warp's last tile.
 bool kv8_attn_fits(const SeqTable& tab, const Kv8Geom& g) {
-    const int64_t slack = ((int64_t)tab.B + 2 * kKv8Batch * kKv8Warps) * kKv8Tile;
+    const int64_t slack = ((int64_t)tab.B * (kKv8RunCost + 1) + 2 * kKv8Batch * kKv8WideWarps) * kKv8Tile;
     return ((int64_t)tab.kept_off[tab.B] << g.c_log2) + slack < (1ll << 31) &&
            ((int64_t)tab.chunk_off[tab.B] << (g.c_log2 + g.h_log2)) < (1ll << 31);
 }

@@ -99,7 +99,7 @@ lsa_status device_info(DeviceInfo* out) {
         int la_occ = 0;
         if (la_init_attrs(&la_occ) != cudaSuccess || la_occ < 1) return LSA_ERR_CUDA;
         di.la_ctas = la_occ * sms;
-        if (kv8_init_attrs(sms, di.kv8_ctas) != cudaSuccess) return LSA_ERR_CUDA;
+        if (kv8_init_attrs(sms, &di.kv8_ctas) != cudaSuccess) return LSA_ERR_CUDA;
         di.ready = true;
     }
     *out = di;
