@@ -23,10 +23,10 @@ cudaError_t launch_kv8_gather(const lsa_dims& d, const SeqTable& tab, const lsa_
                               const int32_t* ids, const int32_t* seq_len, void* K_res, void* V_res, uint32_t* err,
                               cudaStream_t stream);
 bool kv8_attn_fits(const SeqTable& tab, const Kv8Geom& g);
-size_t kv8_part_o_bytes(int ctas);
-size_t kv8_part_ml_bytes(int ctas);
+size_t kv8_part_o_bytes(int num_sms);
+size_t kv8_part_ml_bytes(int num_sms);
 cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv8_cache& cache, const Kv8Geom& g,
-                            int num_sms, int max_ctas, const void* q, const int32_t* ids, const int32_t* counts,
+                            int num_sms, const void* q, const int32_t* ids, const int32_t* counts,
                             const int32_t* seq_len, int len_add, float* part_o, float* part_ml, float* out,
                             float* lse, uint32_t* err, cudaStream_t stream, bool pdl);
 }  // namespace lsa
@@ -65,8 +65,8 @@ Kv8Ws kv8_layout(const lsa_dims* d, const Prepared& p, const DeviceInfo& di) {
     Kv8Ws w;
     w.base = ws_layout(d, p, di);
     w.part_o = w.base.total;
-    w.part_ml = align256(w.part_o + kv8_part_o_bytes(di.kv8_ctas));
-    w.q = align256(w.part_ml + kv8_part_ml_bytes(di.kv8_ctas));
+    w.part_ml = align256(w.part_o + kv8_part_o_bytes(di.sms));
+    w.q = align256(w.part_ml + kv8_part_ml_bytes(di.sms));
     w.total = align256(w.q + (size_t)d->B * d->H * LSA_HEAD_DIM * (d->kv_dtype == LSA_BF16 ? 2 : 4));
     return w;
 }
@@ -218,7 +218,7 @@ lsa_status lsa_kv8_decode_attn(const lsa_dims* dims, const lsa_kv8_cache* cache,
     if (!kv8_attn_fits(c.p.tab, c.g)) return LSA_ERR_UNSUPPORTED;
     s = kv8_device(dims, ws_bytes, &c);
     if (s != LSA_OK) return s;
-    return cuda_status(launch_kv8_attn(*dims, c.p.tab, *cache, c.g, c.di.sms, c.di.kv8_ctas, q, chunk_ids, kept_count, seq_len,
+    return cuda_status(launch_kv8_attn(*dims, c.p.tab, *cache, c.g, c.di.sms, q, chunk_ids, kept_count, seq_len,
                                        0, reinterpret_cast<float*>(at(ws, c.w.part_o)),
                                        reinterpret_cast<float*>(at(ws, c.w.part_ml)), out, lse,
                                        reinterpret_cast<uint32_t*>(ws), static_cast<cudaStream_t>(stream), false));
@@ -268,7 +268,7 @@ lsa_status lsa_decode_step_kv8(const lsa_dims* dims, const lsa_kv8_cache* cache,
         qr = qw;
     }
     if (e == cudaSuccess)
-        e = launch_kv8_attn(*dims, c.p.tab, *cache, c.g, c.di.sms, c.di.kv8_ctas, qr, chunk_ids_out, nullptr, seq_len,
+        e = launch_kv8_attn(*dims, c.p.tab, *cache, c.g, c.di.sms, qr, chunk_ids_out, nullptr, seq_len,
                             k != nullptr ? 1 : 0, reinterpret_cast<float*>(at(ws, c.w.part_o)),
                             reinterpret_cast<float*>(at(ws, c.w.part_ml)), out, lse, err, st, true);
     return cuda_status(e);

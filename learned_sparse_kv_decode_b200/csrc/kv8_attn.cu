@@ -33,34 +33,31 @@
 //    than memory does, so one tile ahead is enough, and few registers (128) matter more. What a warp has
 //    to know of a tile (chunk id, row, scales, how many tokens exist) its lanes work out side by side for
 //    32 groups of 8 tokens ("octets") at a time.
-//  * The tiles of all runs form one list that is split evenly over the CTAs; a CTA joins its warps in
-//    shared memory, and a run that spans CTAs is joined by k_kv8_attn_merge. Runs that one CTA holds
-//    whole are written at once.
+//  * Every run is cut into equal parts, one to a CTA, so that the CTAs fit the device at once; a CTA joins
+//    its warps in shared memory, and the parts of a run are joined by k_kv8_attn_merge. Runs of one part
+//    are written at once.
 #include "kv8.cuh"
 
 namespace lsa {
 
-constexpr int kKv8Warps = 4;       // of a CTA; four CTAs to an SM
-constexpr int kKv8WideWarps = 16;  // of a CTA that holds a short run whole
-constexpr int kKv8WideTiles = 64;  // tiles of the longest run that such a CTA takes
-constexpr int kKv8RunCost = 8;     // what another run costs a CTA, in tiles
 constexpr int kKv8Tile = 32;       // tokens per tile: 4 octets
 constexpr int kKv8Batch = 8;       // tiles whose 32 octets the lanes hold
 constexpr int kKv8MaxRows = 8;     // query heads per run
 constexpr float kKv8PShift = 14.f; // weights are at most 2^14
 constexpr int kKv8SlotV = kKv8Tile * kDh;          // a warp's shared memory: K rows, V rows,
-constexpr int kKv8Meta = 2 * kKv8Tile * kDh;       // a batch's ks[32] and vs / vref [32]
-constexpr int kKv8WarpBytes = kKv8Meta + 2 * 32 * 4;
+constexpr int kKv8Meta = 2 * kKv8Tile * kDh;       // two batches of ks[32], vs / vref [32], n[32]
+constexpr int kKv8MetaBytes = 3 * 32 * 4;
+constexpr int kKv8WarpBytes = kKv8Meta + 2 * kKv8MetaBytes;
 constexpr int kKv8JoinBytes = kKv8MaxRows * (kDh + 2) * 4;  // of a warp; takes the tiles' place
 static_assert(kKv8JoinBytes <= kKv8WarpBytes, "the join's buffers lie where the tiles were");
 __host__ __device__ constexpr int kv8_smem(int sets, int warps) { return warps * kKv8WarpBytes + sets * 4 * 32 * 16; }
 
-// Prefix tables of one call: the kept (or all) chunks and their tiles.
+// Prefix tables of one call: the kept (or all) chunks, and the CTAs (all heads' parts).
 struct Kv8Tab {
     int32_t B;
     int32_t chunk_off[kMaxB + 1];
     int32_t kept_off[kMaxB + 1];
-    int32_t cost_off[kMaxB + 1];  // prefix of the cost of one (sequence, head) run: its tiles + kKv8RunCost
+    int32_t cta_off[kMaxB + 1];
 };
 
 struct Kv8AttnParams {
@@ -72,10 +69,8 @@ struct Kv8AttnParams {
     int32_t H;
     int32_t rows;       // query heads per run: min(group, 8)
     int32_t rts;        // runs per K/V head: group / rows
+    int32_t runs_log2;  // log2 of a sequence's runs, Hkv * rts
     int32_t len_add;    // added to seq_len
-    int32_t G;          // CTAs
-    int32_t by_run;     // a CTA takes one run whole, else an equal share of the cost
-    int64_t F;          // cost of all runs
     float qscale;       // log2(e) / sqrt(Dh)
 };
 
@@ -117,217 +112,193 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void kv8_sts(uint32_t addr, T v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(*reinterpret_cast<const uint32_t*>(&v)) : "memory");
+}
+__device__ __forceinline__ uint32_t kv8_lds(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
 __device__ __forceinline__ uint4 kv8_lds16(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
 
-// a / b for 0 <= a, 0 < b: in 32 bits where both fit, which is nearly always.
-__device__ __forceinline__ int64_t kv8_div(int64_t a, int64_t b) {
-    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
-
-// The CTA whose range [c F / G, (c + 1) F / G) holds unit u.
-__device__ __forceinline__ int kv8_cta_of(int64_t u, int64_t F, int G) {
-    return (int)(kv8_div((u + 1) * G + F - 1, F) - 1);
-}
-
-// The sequence whose runs hold unit u.
-__device__ __forceinline__ int kv8_seq_of(const Kv8Tab& tab, int runs_b, int64_t u) {
+// The sequence whose CTAs hold CTA c.
+__device__ __forceinline__ int kv8_seq_of(const Kv8Tab& tab, int c) {
     int lo = 0, hi = tab.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)tab.cost_off[mid] * runs_b <= u) lo = mid; else hi = mid - 1;
+        if (tab.cta_off[mid] <= c) lo = mid; else hi = mid - 1;
     }
     return lo;
 }
 
-// One lane's octet of a batch: its first row in the cache (in rows of Dh bytes), how many of its 8
-// tokens take part, its scales.
-struct Kv8Octet {
-    uint32_t row;
-    int n;
-    float ks, vs;
-};
-
-// grid G, WARPS * 32 threads. SETS: products of S, two terms of q each (bf16: 1, fp32: 3); PLO: groups
-// of 8 (a second product for P's low halves).
+// Grid: all parts of all runs; WARPS * 32 threads. SETS: products of S, two terms of q each (bf16: 1,
+// fp32: 3); PLO: groups of 8 (a second product for P's low halves).
 template <int SETS, bool PLO, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     extern __shared__ __align__(128) uint8_t smem[];
-    float(*s_o)[kKv8MaxRows][kDh] = reinterpret_cast<float(*)[kKv8MaxRows][kDh]>(smem);
-    float(*s_ml)[kKv8MaxRows][2] =
-        reinterpret_cast<float(*)[kKv8MaxRows][2]>(smem + WARPS * kKv8MaxRows * kDh * 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int runs_b = p.g.Hkv * p.rts;
-    const int my_row = g & (p.rows - 1);
     const int c_log2 = p.g.c_log2;
-    const bool contig = c_log2 >= 5;  // a tile's octets follow one another in the cache
-    const uint32_t slot = smem_u32(smem) + warp * kKv8WarpBytes, meta = slot + kKv8Meta;
-    const uint32_t qs = smem_u32(smem) + WARPS * kKv8WarpBytes + lane * 16;  // q's terms: [set][step][lane]
-    // A row's 16-byte units are XOR-swizzled by the row: the copies' and both fragments' accesses are
-    // free of bank conflicts. Offsets of this lane within an octet (8 rows, 1 KB):
-    const uint32_t cp0 = (lane >> 3) * kDh + (((lane & 7) ^ (lane >> 3)) << 4);
-    const uint32_t cp1 = ((lane >> 3) + 4) * kDh + (((lane & 7) ^ ((lane >> 3) + 4)) << 4);
-    const uint32_t k_at0 = g * kDh + ((2 * t ^ g) << 4), k_at1 = g * kDh + (((2 * t + 1) ^ g) << 4);
-    const uint32_t v_at0 = kKv8SlotV + 2 * t * kDh + ((g ^ 2 * t) << 4);
-    const uint32_t v_at1 = kKv8SlotV + (2 * t + 1) * kDh + ((g ^ (2 * t + 1)) << 4);
     pdl_trigger();
-    pdl_wait();
 
-    // This CTA's cost units. A run's first kKv8RunCost units are what beginning it costs; its tiles follow.
-    int b;
-    int64_t u0, u1;
-    if (p.by_run) {
-        b = blockIdx.x / runs_b;
-        const int cost = tab.cost_off[b + 1] - tab.cost_off[b];
-        u0 = (int64_t)tab.cost_off[b] * runs_b + (int64_t)(blockIdx.x - b * runs_b) * cost;
-        u1 = u0 + cost;
-    } else {
-        u0 = kv8_div((int64_t)blockIdx.x * p.F, p.G);
-        u1 = kv8_div(((int64_t)blockIdx.x + 1) * p.F, p.G);
-        b = kv8_seq_of(tab, runs_b, u0);
+    // ---- this CTA's part: a sequence's CTAs are ordered by part, then run
+    const int b = kv8_seq_of(tab, blockIdx.x);
+    const int idx = blockIdx.x - tab.cta_off[b], run = idx & ((1 << p.runs_log2) - 1), part = idx >> p.runs_log2;
+    const int parts = (tab.cta_off[b + 1] - tab.cta_off[b]) >> p.runs_log2;
+    const int h = run / p.rts;
+    const int qrow0 = b * p.H + run * p.rows;
+    int tile0, tile1;
+    {
+        const int tokens = (tab.kept_off[b + 1] - tab.kept_off[b]) << c_log2;
+        const int tiles = (tokens + kKv8Tile - 1) / kKv8Tile, per = tiles / parts, more = tiles - per * parts;
+        tile0 = part * per + min(part, more);
+        tile1 = tile0 + per + (part < more ? 1 : 0);
     }
-    for (int64_t u = u0; u < u1;) {
-        // ---- the run that holds unit u
-        while (u >= (int64_t)tab.cost_off[b + 1] * runs_b) ++b;
-        const int cost = tab.cost_off[b + 1] - tab.cost_off[b];
-        const int64_t rel = u - (int64_t)tab.cost_off[b] * runs_b;
-        const int run = (int)kv8_div(rel, cost);
-        const int from = (int)(rel - (int64_t)run * cost);
-        const int to = (int)min((int64_t)cost, from + (u1 - u));
-        const int tile0 = max(from - kKv8RunCost, 0), tile1 = max(to - kKv8RunCost, 0);
-        const bool all = from == 0 && to == cost;
-        const int64_t part = 2 * (int64_t)blockIdx.x + (u == u0 ? 0 : 1);  // where a part of a run is left
-        u += to - from;
-        if (!all && tile0 == tile1) {  // only of the beginning's cost
-            if (tid < p.rows) {
-                p.part_ml[(part * kKv8MaxRows + tid) * 2] = -INFINITY;
-                p.part_ml[(part * kKv8MaxRows + tid) * 2 + 1] = 0.f;
-            }
-            continue;
-        }
-        const int h = run / p.rts, rt = run - h * p.rts;
-        const int n_b = tab.chunk_off[b + 1] - tab.chunk_off[b];
-        int kept = tab.kept_off[b + 1] - tab.kept_off[b];
-        const int32_t* ids = p.ids != nullptr ? p.ids + tab.kept_off[b] : nullptr;
-        if (p.counts != nullptr) kept = max(0, min(kept, p.counts[b]));
-        int64_t len = (int64_t)n_b << c_log2;
-        if (p.seq_len != nullptr) len = max((int64_t)0, min(len, (int64_t)p.seq_len[b] + p.len_add));
-        if (ids == nullptr) kept = min(kept, (int)((len + (1 << c_log2) - 1) >> c_log2));
-        const int qrow0 = b * p.H + (h * p.rts + rt) * p.rows;
-        // This warp's tiles are tile0 + warp + WARPS * i, i < n_it, as far as there are tokens.
-        const int last = min(tile1, (int)((((int64_t)kept << c_log2) + kKv8Tile - 1) / kKv8Tile));
-        const int n_it = (max(last - tile0 - warp, 0) + WARPS - 1) / WARPS;
+    pdl_wait();
+    // chunks and tokens that take part (both fit in 31 bits)
+    int kept = tab.kept_off[b + 1] - tab.kept_off[b];
+    int len = (tab.chunk_off[b + 1] - tab.chunk_off[b]) << c_log2;
+    if (p.counts != nullptr) kept = max(0, min(kept, p.counts[b]));
+    if (p.seq_len != nullptr) {
+        const int n = p.seq_len[b];  // + len_add may pass 2^31 - 1
+        len = n >= len ? len : max(0, min(len, n + p.len_add));
+    }
+    if (p.ids == nullptr) kept = min(kept, (len + (1 << c_log2) - 1) >> c_log2);
+    // This warp's tiles are tile0 + warp + WARPS * i, i < n_it, as far as there are tokens.
+    const int first = tile0 + warp;
+    const int n_it = (max(min(tile1, ((kept << c_log2) + kKv8Tile - 1) / kKv8Tile) - first, 0) + WARPS - 1) / WARPS;
 
-        // ---- what the lanes know of the octets: lane L has octet L % 4 of tile (batch) + L / 4
-        Kv8Octet oct = {0, 0, 0.f, 0.f};  // of the tiles being copied
-        uint32_t nz = 0;                  // octets (lanes) with tokens
-        int id_next = 0;
-        auto token_of = [&](int i) {      // first token of this lane's octet in the batch of tile i
-            return (tile0 + warp + WARPS * (i + (lane >> 2))) * kKv8Tile + 8 * (lane & 3);
-        };
-        auto fetch_id = [&](int i) {
-            const int j = token_of(i) >> c_log2;
-            id_next = j >= kept ? -1 : ids != nullptr ? ids[j] : j;
-        };
-        auto next_batch = [&](int i) {
-            const int tk = token_of(i), j = tk >> c_log2, w = tk & ((1 << c_log2) - 1), id = id_next;
-            oct.n = 0;
-            oct.ks = oct.vs = 0.f;
-            if (j < kept && i + (lane >> 2) < n_it) {
-                if (id >= 0 && id < n_b) {
-                    const int64_t left = len - (((int64_t)id << c_log2) + w);
-                    oct.n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
-                    const int64_t ch = (int64_t)(tab.chunk_off[b] + id) * p.g.Hkv + h;
-                    oct.row = (uint32_t)((ch << c_log2) + w);
-                    if (oct.n > 0) {
-                        const int64_t si = ch * p.g.spc + (w >> p.g.sb_log2);
-                        oct.ks = p.k_scale[si];
-                        oct.vs = p.v_scale[si];
-                    }
-                } else {
-                    set_error(err, kErrBadId);
+    // ---- addresses in shared memory. A row's 16-byte units are XOR-swizzled by the row: the copies' and
+    // both fragments' accesses are free of bank conflicts.
+    const uint32_t slot = smem_u32(smem) + warp * kKv8WarpBytes, meta = slot + kKv8Meta + 4 * lane;
+    const uint32_t cp0 = slot + (lane >> 3) * kDh + (((lane & 7) ^ (lane >> 3)) << 4);
+    const uint32_t cp1 = slot + ((lane >> 3) + 4) * kDh + (((lane & 7) ^ ((lane >> 3) + 4)) << 4);
+    const uint32_t ka0 = slot + g * kDh + ((2 * t ^ g) << 4), ka1 = ka0 ^ 16;
+    const uint32_t va0 = slot + kKv8SlotV + 2 * t * kDh + ((g ^ 2 * t) << 4);
+    const uint32_t va1 = slot + kKv8SlotV + (2 * t + 1) * kDh + ((g ^ (2 * t + 1)) << 4);
+    const uint32_t qs = smem_u32(smem) + WARPS * kKv8WarpBytes + lane * 16;  // q's terms: [set][step][lane]
+
+    // ---- what the lanes know of the octets being copied: lane L has octet L % 4 of tile (batch) + L / 4.
+    // Its first row in the cache stays in a register; its scales and its count of tokens that take part go
+    // to the batch's place in shared memory, for when the batch is read.
+    uint32_t row = 0;
+    uint32_t nz = 0;  // octets (lanes) with tokens
+    int id_next = 0;
+    auto token_of = [&](int i) {  // first token of this lane's octet in the batch of tile i
+        return (first + WARPS * (i + (lane >> 2))) * kKv8Tile + 8 * (lane & 3);
+    };
+    auto fetch_id = [&](int i) {
+        const int j = token_of(i) >> c_log2;
+        id_next = j >= kept ? -1 : p.ids != nullptr ? p.ids[tab.kept_off[b] + j] : j;
+    };
+    auto next_batch = [&](int i) {
+        const int tk = token_of(i), w = tk & ((1 << c_log2) - 1), id = id_next;
+        const uint32_t m = meta + (i & kKv8Batch ? kKv8MetaBytes : 0);
+        int n = 0;
+        if (tk >> c_log2 < kept && i + (lane >> 2) < n_it) {
+            if (id >= 0 && id < tab.chunk_off[b + 1] - tab.chunk_off[b]) {
+                n = min(max(len - ((id << c_log2) + w), 0), 8);
+                const uint32_t ch = (uint32_t)(tab.chunk_off[b] + id) * p.g.Hkv + h;
+                row = (ch << c_log2) + w;
+                if (n > 0) {
+                    const uint32_t si = ch * p.g.spc + (w >> p.g.sb_log2);
+                    cp_async4(m, p.k_scale + si);
+                    cp_async4(m + 128, p.v_scale + si);
                 }
+            } else {
+                set_error(err, kErrBadId);
             }
-            nz = __ballot_sync(0xffffffffu, oct.n > 0);
-            fetch_id(i + kKv8Batch);
-        };
-        // Copies of tile i's K or V rows, one group for each (empty past the end). Octets without tokens
-        // are not copied; of the others all 8 rows are (they lie in the cache).
-        auto copy = [&](int i, const uint8_t* base, uint32_t dst) {
-            if (i < n_it) {
-                const int l0 = 4 * (i & (kKv8Batch - 1));
-                if (contig) {  // if the first octet has no tokens, the later ones have none either
-                    const uint32_t row = __shfl_sync(0xffffffffu, oct.row, l0);
-                    if (nz >> l0 & 1) {
-                        const uint8_t* src = base + (uint64_t)row * kDh + lane * 16;
-#pragma unroll
-                        for (int o = 0; o < 4; ++o) {
-                            cp_async16(dst + cp0 + o * 8 * kDh, src + o * 8 * kDh);
-                            cp_async16(dst + cp1 + o * 8 * kDh, src + o * 8 * kDh + 4 * kDh);
-                        }
-                    }
-                } else {
+        }
+        if (n == 0) {
+            kv8_sts(m, 0.f);
+            kv8_sts(m + 128, 0.f);
+        }
+        kv8_sts(m + 256, n);
+        nz = __ballot_sync(0xffffffffu, n > 0);
+        fetch_id(i + kKv8Batch);
+    };
+    // Copies of tile i's K or V rows (`off` into the warp's tile), one group for each (empty past the end).
+    // Octets without tokens are not copied; of the others all 8 rows are (they lie in the cache).
+    auto copy = [&](int i, const uint8_t* base, uint32_t off) {
+        if (i < n_it) {
+            const int l0 = 4 * (i & (kKv8Batch - 1));
+            if (c_log2 >= 5) {  // the octets follow one another; if the first has no tokens, nor have the others
+                const uint32_t r = __shfl_sync(0xffffffffu, row, l0);
+                if (nz >> l0 & 1) {
+                    const uint8_t* src = base + (uint64_t)r * kDh + lane * 16;
 #pragma unroll
                     for (int o = 0; o < 4; ++o) {
-                        const uint32_t row = __shfl_sync(0xffffffffu, oct.row, l0 + o);
-                        if (nz >> (l0 + o) & 1) {
-                            const uint8_t* src = base + (uint64_t)row * kDh + lane * 16;
-                            cp_async16(dst + cp0 + o * 8 * kDh, src);
-                            cp_async16(dst + cp1 + o * 8 * kDh, src + 4 * kDh);
-                        }
+                        cp_async16(cp0 + off + o * 8 * kDh, src + o * 8 * kDh);
+                        cp_async16(cp1 + off + o * 8 * kDh, src + o * 8 * kDh + 4 * kDh);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int o = 0; o < 4; ++o) {
+                    const uint32_t r = __shfl_sync(0xffffffffu, row, l0 + o);
+                    if (nz >> (l0 + o) & 1) {
+                        const uint8_t* src = base + (uint64_t)r * kDh + lane * 16;
+                        cp_async16(cp0 + off + o * 8 * kDh, src);
+                        cp_async16(cp1 + off + o * 8 * kDh, src + 4 * kDh);
                     }
                 }
             }
-            cp_async_commit();
+        }
+        cp_async_commit();
+    };
+
+    fetch_id(0);
+    next_batch(0);
+    copy(0, p.K8, 0);
+    copy(0, p.V8, kKv8SlotV);
+
+    // ---- q: row g % rows, scaled to stay below 256, as e4m3 terms worth 16^-i; each of four warps does a
+    // step's share of the 128 values (8 per lane)
+    float qmul;
+    {
+        const int64_t at = (int64_t)(qrow0 + (g & (p.rows - 1))) * kDh + t * 32;
+        auto load = [&](int i, float* x) {  // values 8 i .. 8 i + 7 of the lane's 32
+            constexpr bool BF16 = SETS == 1;
+            octet_floats<BF16>(octet_load<BF16>(p.q + at * (BF16 ? 2 : 4), i), x);
         };
-
-        fetch_id(0);
-        next_batch(0);
-        copy(0, p.K8, slot);
-        copy(0, p.V8, slot + kKv8SlotV);
-
-        // ---- q: row my_row, scaled to stay below 256, as e4m3 terms worth 16^-i; each of four warps
-        // does a step's share of the 128 values (8 per lane)
-        float qmul;
-        {
-            const int64_t at = (int64_t)(qrow0 + my_row) * kDh + t * 32;
-            auto load = [&](int i, float* x) {  // values 8 i .. 8 i + 7 of the lane's 32
-                constexpr bool BF16 = SETS == 1;
-                octet_floats<BF16>(octet_load<BF16>(p.q + at * (BF16 ? 2 : 4), i), x);
-            };
-            float top = 0.f;
-            bool nan = false;
+        float top = 0.f;
+        bool nan = false;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                float x[8];
-                load(s, x);
+        for (int s = 0; s < 4; ++s) {
+            float x[8];
+            load(s, x);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    top = fmaxf(top, fabsf(x[e]));
-                    nan |= x[e] != x[e];
-                }
+            for (int e = 0; e < 8; ++e) {
+                top = fmaxf(top, fabsf(x[e]));
+                nan |= x[e] != x[e];
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // top < 2^(ex + 1): times 2^(7 - ex) it stays below 2^8. The factor is kept within fp32.
-            int ex = (int)(__float_as_uint(top) >> 23) - 127;
-            ex = ex < -110 ? -110 : ex;
-            const float up = __uint_as_float((uint32_t)(7 - ex + 127) << 23);
-            qmul = p.qscale * __uint_as_float((uint32_t)(ex - 7 + 127) << 23);
-            // a row with an infinity or a NaN has no finite scores
-            const uint32_t bad = __ballot_sync(0xffffffffu, nan || !(top < INFINITY));
-            if (bad >> (lane & 28) & 15) qmul = __uint_as_float(0x7fc00000u);
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // top < 2^(ex + 1): times 2^(7 - ex) it stays below 2^8. The factor is kept within fp32.
+        int ex = (int)(__float_as_uint(top) >> 23) - 127;
+        ex = ex < -110 ? -110 : ex;
+        const float up = __uint_as_float((uint32_t)(7 - ex + 127) << 23);
+        qmul = p.qscale * __uint_as_float((uint32_t)(ex - 7 + 127) << 23);
+        // a row with an infinity or a NaN has no finite scores
+        const uint32_t bad = __ballot_sync(0xffffffffu, nan || !(top < INFINITY));
+        if (bad >> (lane & 28) & 15) qmul = __uint_as_float(0x7fc00000u);
+        if (warp < 4) {
             float y[8];
-            load(warp & 3, y);
+            load(warp, y);
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] *= up;
 #pragma unroll
-            for (int k = 0; k < SETS && warp < 4; ++k) {
+            for (int k = 0; k < SETS; ++k) {
                 uint32_t a[4];  // the 16-row operand's registers: term 2 k in rows 0..7, 2 k + 1 in rows 8..15
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -346,273 +317,246 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
                              : "memory");
             }
         }
-        __syncthreads();
+    }
+    __syncthreads();
 
-        float o[8][4], m = -INFINITY, l = 0.f, vref = 0.f;
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t full = 0;  // octets of the batch in use whose 8 tokens all take part
-        int n = 0;          // tokens of this lane's octet of that batch
+    float o[8][4], m = -INFINITY, l = 0.f, vref = 0.f;
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    uint32_t full = 0;  // octets of the batch in use whose 8 tokens all take part
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-        for (int it = 0; it < n_it; ++it) {
-            const int l0 = 4 * (it & (kKv8Batch - 1));
-            float vf = 1.f;
-            if (l0 == 0) {  // a new batch: its scales, and V's reference, which it may raise
-                n = oct.n;
-                full = __ballot_sync(0xffffffffu, n == 8);
-                float vtop = oct.vs;
+    for (int it = 0; it < n_it; ++it) {
+        const int l0 = 4 * (it & (kKv8Batch - 1));
+        const uint32_t mt = meta + (it & kKv8Batch ? kKv8MetaBytes : 0);  // this batch's, at this lane
+        cp_async_wait<1>();
+        __syncwarp();  // every lane's copies of K have landed
+        float vf = 1.f;
+        if (l0 == 0) {  // a new batch: its scales, and V's reference, which it may raise
+            full = __ballot_sync(0xffffffffu, kv8_lds(mt + 256) == 8);
+            const float vs = __uint_as_float(kv8_lds(mt + 128));
+            float vtop = vs;
 #pragma unroll
-                for (int k = 1; k < 32; k <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, k));
-                if (vtop > vref && vtop >= 1.17549435e-38f) {
-                    vf = vref / vtop;
-                    vref = vtop;
-                }
-                const float rv = vref > 0.f ? oct.vs / vref : 0.f;
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(meta + 4 * lane), "f"(oct.ks) : "memory");
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(meta + 128 + 4 * lane), "f"(rv) : "memory");
+            for (int k = 1; k < 32; k <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, k));
+            if (vtop > vref && vtop >= 1.17549435e-38f) {
+                vf = vref / vtop;
+                vref = vtop;
             }
-            const bool whole = (full >> l0 & 15u) == 15u;
+            kv8_sts(mt + 128, vref > 0.f ? vs / vref : 0.f);  // read behind the next barrier
+        }
+        const bool whole = (full >> l0 & 15u) == 15u;
+        const uint32_t mb = mt - 4 * lane + 4 * l0;  // of the tile's four octets
 
-            // ---- S: the terms of q against the tile's tokens
-            cp_async_wait<1>();
-            __syncwarp();  // every lane's copies of K have landed
-            float sc[8];
-            {
-                const uint4 k4 = kv8_lds16(meta + 4 * l0);
-                const float ks[4] = {__uint_as_float(k4.x), __uint_as_float(k4.y), __uint_as_float(k4.z),
-                                     __uint_as_float(k4.w)};
-                constexpr int OC = SETS == 1 ? 4 : 2;  // octets at a time: what the registers hold
+        // ---- S: the terms of q against the tile's tokens
+        float sc[8];
+        {
+            constexpr int OC = SETS == 1 ? 4 : 2;  // octets at a time: what the registers hold
 #pragma unroll
-                for (int i0 = 0; i0 < 4; i0 += OC) {
-                    uint32_t kw[OC][8];
+            for (int i0 = 0; i0 < 4; i0 += OC) {
+                if (SETS > 1) __syncwarp();  // keeps the second half's loads from moving up
+                uint32_t kw[OC][8];
 #pragma unroll
-                    for (int i = 0; i < OC; ++i) {
-                        const uint4 ka = kv8_lds16(slot + k_at0 + (i0 + i) * 8 * kDh);
-                        const uint4 kb = kv8_lds16(slot + k_at1 + (i0 + i) * 8 * kDh);
-                        kw[i][0] = ka.x; kw[i][1] = ka.y; kw[i][2] = ka.z; kw[i][3] = ka.w;
-                        kw[i][4] = kb.x; kw[i][5] = kb.y; kw[i][6] = kb.z; kw[i][7] = kb.w;
-                    }
+                for (int i = 0; i < OC; ++i) {
+                    const uint4 ka = kv8_lds16(ka0 + (i0 + i) * 8 * kDh), kb = kv8_lds16(ka1 + (i0 + i) * 8 * kDh);
+                    kw[i][0] = ka.x; kw[i][1] = ka.y; kw[i][2] = ka.z; kw[i][3] = ka.w;
+                    kw[i][4] = kb.x; kw[i][5] = kb.y; kw[i][6] = kb.z; kw[i][7] = kb.w;
+                }
 #pragma unroll
-                    for (int k = SETS - 1; k >= 0; --k) {
-                        float c[OC][4];
+                for (int k = SETS - 1; k >= 0; --k) {
+                    float c[OC][4];
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            const uint4 a = kv8_lds16(qs + (k * 4 + s) * 512);
-#pragma unroll
-                            for (int i = 0; i < OC; ++i) {
-                                if (s == 0) mma_e4m3(c[i], a, kw[i][0], kw[i][1], zero);
-                                else mma_e4m3(c[i], a, kw[i][2 * s], kw[i][2 * s + 1], c[i]);
-                            }
-                        }
+                    for (int s = 0; s < 4; ++s) {
+                        const uint4 a = kv8_lds16(qs + (k * 4 + s) * 512);
 #pragma unroll
                         for (int i = 0; i < OC; ++i) {
+                            if (s == 0) mma_e4m3(c[i], a, kw[i][0], kw[i][1], zero);
+                            else mma_e4m3(c[i], a, kw[i][2 * s], kw[i][2 * s + 1], c[i]);
+                        }
+                    }
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float& y = sc[2 * (i0 + i) + e];
-                                const float hi = k == SETS - 1 ? c[i][2 + e] : fmaf(y, 0.0625f, c[i][2 + e]);
-                                y = fmaf(hi, 0.0625f, c[i][e]);
-                            }
+                    for (int i = 0; i < OC; ++i) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float& y = sc[2 * (i0 + i) + e];
+                            const float hi = k == SETS - 1 ? c[i][2 + e] : fmaf(y, 0.0625f, c[i][2 + e]);
+                            y = fmaf(hi, 0.0625f, c[i][e]);
                         }
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float f = qmul * ks[i];
-                    sc[2 * i] *= f;
-                    sc[2 * i + 1] *= f;
-                }
             }
-            if (!whole) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int ni = __shfl_sync(0xffffffffu, n, l0 + i);
-                    if (2 * t >= ni) sc[2 * i] = -INFINITY;
-                    if (2 * t + 1 >= ni) sc[2 * i + 1] = -INFINITY;
-                }
-            }
-            __syncwarp();  // the K rows are read
-            if ((it + 1) % kKv8Batch == 0) next_batch(it + 1);
-            copy(it + 1, p.K8, slot);
-
-            // ---- running maximum of row my_row
-            float mx = m;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mx = fmaxf(mx, sc[i]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float ref = mx == -INFINITY ? 0.f : mx;
-            const float al = kv8_ex2(m - ref);
-            m = mx;
-            const float a0 = __shfl_sync(0xffffffffu, al, 8 * t) * vf;  // of columns 2 t and 2 t + 1
-            const float a1 = __shfl_sync(0xffffffffu, al, 8 * t + 4) * vf;
-            // ---- weights (times 2^14, which out = O / l cancels) and their f16 halves
-            const float ms = ref - kKv8PShift;
-            uint32_t ph[4], pl[PLO ? 4 : 1];
-            {
-                const uint4 r4 = kv8_lds16(meta + 128 + 4 * l0);
-                const float rv[4] = {__uint_as_float(r4.x), __uint_as_float(r4.y), __uint_as_float(r4.z),
-                                     __uint_as_float(r4.w)};
-                float ls = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p0 = kv8_ex2(sc[2 * i] - ms), p1 = kv8_ex2(sc[2 * i + 1] - ms);
-                    ls += p0 + p1;
-                    const float w0 = p0 * rv[i], w1 = p1 * rv[i];
-                    ph[i] = f16x2_rn(w0, w1);
-                    const float2 f = f16x2_floats(ph[i]);
-                    const uint32_t low = f16x2_rn(w0 - f.x, w1 - f.y);
-                    if constexpr (PLO) pl[i] = low;
-                    else ph[i] = g >= 4 ? low : ph[i];  // columns 4..7 carry the low halves of columns 0..3
-                }
-                l = fmaf(l, al, ls);
-            }
-
-            // ---- O^T = O^T alpha + V^T P^T
-            cp_async_wait<1>();
-            __syncwarp();  // every lane's copies of V have landed
-            uint4 vv[8];
+            const uint4 k4 = kv8_lds16(mb);
+            const uint32_t ks[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                vv[2 * i] = kv8_lds16(slot + v_at0 + i * 8 * kDh);
-                vv[2 * i + 1] = kv8_lds16(slot + v_at1 + i * 8 * kDh);
+                const float f = qmul * __uint_as_float(ks[i]);
+                sc[2 * i] *= f;
+                sc[2 * i + 1] *= f;
             }
-            if (!whole) {  // rows behind the sequence may hold anything: a weight of 0 does not undo a NaN
+        }
+        if (!whole) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int ni = __shfl_sync(0xffffffffu, n, l0 + i);
-                    if (2 * t >= ni) vv[2 * i] = make_uint4(0, 0, 0, 0);
-                    if (2 * t + 1 >= ni) vv[2 * i + 1] = make_uint4(0, 0, 0, 0);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int n = (int)kv8_lds(mb + 256 + 4 * i);
+                if (2 * t >= n) sc[2 * i] = -INFINITY;
+                if (2 * t + 1 >= n) sc[2 * i + 1] = -INFINITY;
             }
-            __syncwarp();  // the V rows are read
-            copy(it + 1, p.V8, slot + kKv8SlotV);
+        }
+        __syncwarp();  // the K rows are read
+        if ((it + 1) % kKv8Batch == 0) next_batch(it + 1);
+        copy(it + 1, p.K8, 0);
+
+        // ---- running maximum of the lane's row of q
+        float mx = m;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, sc[i]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        const float al = kv8_ex2(m - ref);
+        m = mx;
+        const float a0 = __shfl_sync(0xffffffffu, al, 8 * t) * vf;  // of columns 2 t and 2 t + 1
+        const float a1 = __shfl_sync(0xffffffffu, al, 8 * t + 4) * vf;
+        // ---- weights (times 2^14, which out = O / l cancels) and their f16 halves
+        const float ms = ref - kKv8PShift;
+        uint32_t ph[4], pl[PLO ? 4 : 1];
+        {
+            const uint4 r4 = kv8_lds16(mb + 128);
+            const uint32_t rv[4] = {r4.x, r4.y, r4.z, r4.w};
+            float ls = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float c[4];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {  // tokens 0..15, 16..31 of the tile
-                        const uint32_t y0 = __byte_perm((&vv[4 * e].x)[w], (&vv[4 * e + 1].x)[w], i ? 0x7362 : 0x5140);
-                        const uint32_t y1 = __byte_perm((&vv[4 * e + 2].x)[w], (&vv[4 * e + 3].x)[w], i ? 0x7362 : 0x5140);
-                        const uint32_t b0 = e4m3lo_f16x2(y0), b1 = e4m3hi_f16x2(y0);
-                        const uint32_t b2 = e4m3lo_f16x2(y1), b3 = e4m3hi_f16x2(y1);
-                        if (e == 0) mma_f16(c, b0, b1, b2, b3, ph[0], ph[1], zero);
-                        else mma_f16(c, b0, b1, b2, b3, ph[2], ph[3], c);
-                        if constexpr (PLO) mma_f16(c, b0, b1, b2, b3, pl[2 * e], pl[2 * e + 1], c);
-                    }
-                    float(&oo)[4] = o[2 * w + i];
-                    oo[0] = fmaf(oo[0], a0, c[0]);
-                    oo[1] = fmaf(oo[1], a1, c[1]);
-                    oo[2] = fmaf(oo[2], a0, c[2]);
-                    oo[3] = fmaf(oo[3], a1, c[3]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float p0 = kv8_ex2(sc[2 * i] - ms), p1 = kv8_ex2(sc[2 * i + 1] - ms);
+                ls += p0 + p1;
+                const float w0 = p0 * __uint_as_float(rv[i]), w1 = p1 * __uint_as_float(rv[i]);
+                ph[i] = f16x2_rn(w0, w1);
+                const float2 f = f16x2_floats(ph[i]);
+                const uint32_t low = f16x2_rn(w0 - f.x, w1 - f.y);
+                if constexpr (PLO) pl[i] = low;
+                else ph[i] = g >= 4 ? low : ph[i];  // columns 4..7 carry the low halves of columns 0..3
             }
+            l = fmaf(l, al, ls);
         }
 
-        // ---- join the warps
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if constexpr (!PLO) {
+        // ---- O^T = O^T alpha + V^T P^T
+        cp_async_wait<1>();
+        __syncwarp();  // every lane's copies of V have landed
+        uint4 vv[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[j][e] += __shfl_xor_sync(0xffffffffu, o[j][e], 2);
+        for (int i = 0; i < 4; ++i) {
+            vv[2 * i] = kv8_lds16(va0 + i * 8 * kDh);
+            vv[2 * i + 1] = kv8_lds16(va1 + i * 8 * kDh);
         }
-        cp_async_wait<0>();
-        __syncthreads();  // the tiles are done with
-        if (t == 0 && g < p.rows) {
-            s_ml[warp][g][0] = m == -INFINITY ? -INFINITY : m - kKv8PShift;
-            s_ml[warp][g][1] = l;
-        }
+        if (!whole) {  // rows behind the sequence may hold anything: a weight of 0 does not undo a NaN
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = 2 * t + e;
-            if (row < p.rows) {
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    *reinterpret_cast<float4*>(&s_o[warp][row][16 * g + 4 * w]) =
-                        make_float4(o[2 * w][e] * vref, o[2 * w][2 + e] * vref, o[2 * w + 1][e] * vref,
-                                    o[2 * w + 1][2 + e] * vref);
+            for (int i = 0; i < 4; ++i) {
+                const int n = (int)kv8_lds(mb + 256 + 4 * i);
+                if (2 * t >= n) vv[2 * i] = make_uint4(0, 0, 0, 0);
+                if (2 * t + 1 >= n) vv[2 * i + 1] = make_uint4(0, 0, 0, 0);
             }
         }
-        __syncthreads();
-        for (int i = tid; i < p.rows * kDh; i += WARPS * 32) {
-            const int row = i >> 7, d = i & (kDh - 1);
-            float M = -INFINITY, A = 0.f, L = 0.f;
+        __syncwarp();  // the V rows are read
+        copy(it + 1, p.V8, kKv8SlotV);
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][row][0]);
+        for (int w = 0; w < 4; ++w) {
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float mw = s_ml[w][row][0];
-                const float f = mw == -INFINITY ? 0.f : kv8_ex2(mw - M);
-                A = fmaf(f, s_o[w][row][d], A);
-                L = fmaf(f, s_ml[w][row][1], L);
-            }
-            if (all) {
-                p.out[(int64_t)(qrow0 + row) * kDh + d] = L == 0.f ? 0.f : A / L;
-                if (d == 0 && p.lse != nullptr)
-                    p.lse[qrow0 + row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-            } else {
-                p.part_o[(part * kKv8MaxRows + row) * kDh + d] = A;
-                if (d == 0) {
-                    p.part_ml[(part * kKv8MaxRows + row) * 2] = M;
-                    p.part_ml[(part * kKv8MaxRows + row) * 2 + 1] = L;
+            for (int i = 0; i < 2; ++i) {
+                float c[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // tokens 0..15, 16..31 of the tile
+                    const uint32_t y0 = __byte_perm((&vv[4 * e].x)[w], (&vv[4 * e + 1].x)[w], i ? 0x7362 : 0x5140);
+                    const uint32_t y1 = __byte_perm((&vv[4 * e + 2].x)[w], (&vv[4 * e + 3].x)[w], i ? 0x7362 : 0x5140);
+                    const uint32_t b0 = e4m3lo_f16x2(y0), b1 = e4m3hi_f16x2(y0);
+                    const uint32_t b2 = e4m3lo_f16x2(y1), b3 = e4m3hi_f16x2(y1);
+                    if (e == 0) mma_f16(c, b0, b1, b2, b3, ph[0], ph[1], zero);
+                    else mma_f16(c, b0, b1, b2, b3, ph[2], ph[3], c);
+                    if constexpr (PLO) mma_f16(c, b0, b1, b2, b3, pl[2 * e], pl[2 * e + 1], c);
                 }
+                float(&oo)[4] = o[2 * w + i];
+                oo[0] = fmaf(oo[0], a0, c[0]);
+                oo[1] = fmaf(oo[1], a1, c[1]);
+                oo[2] = fmaf(oo[2], a0, c[2]);
+                oo[3] = fmaf(oo[3], a1, c[3]);
             }
         }
-        __syncthreads();  // the shared partials are free for the next run
+    }
+
+    // ---- join the warps
+    float(*s_o)[kKv8MaxRows][kDh] = reinterpret_cast<float(*)[kKv8MaxRows][kDh]>(smem);
+    float(*s_ml)[kKv8MaxRows][2] = reinterpret_cast<float(*)[kKv8MaxRows][2]>(smem + WARPS * kKv8MaxRows * kDh * 4);
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if constexpr (!PLO) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] += __shfl_xor_sync(0xffffffffu, o[j][e], 2);
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // the tiles are done with
+    if (t == 0 && g < p.rows) {
+        s_ml[warp][g][0] = m == -INFINITY ? -INFINITY : m - kKv8PShift;
+        s_ml[warp][g][1] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = 2 * t + e;
+        if (r < p.rows) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                *reinterpret_cast<float4*>(&s_o[warp][r][16 * g + 4 * w]) =
+                    make_float4(o[2 * w][e] * vref, o[2 * w][2 + e] * vref, o[2 * w + 1][e] * vref,
+                                o[2 * w + 1][2 + e] * vref);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < p.rows * kDh; i += WARPS * 32) {
+        const int r = i >> 7, d = i & (kDh - 1);
+        float M = -INFINITY, A = 0.f, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][r][0]);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float mw = s_ml[w][r][0];
+            const float f = mw == -INFINITY ? 0.f : kv8_ex2(mw - M);
+            A = fmaf(f, s_o[w][r][d], A);
+            L = fmaf(f, s_ml[w][r][1], L);
+        }
+        if (parts == 1) {
+            p.out[(int64_t)(qrow0 + r) * kDh + d] = L == 0.f ? 0.f : A / L;
+            if (d == 0 && p.lse != nullptr)
+                p.lse[qrow0 + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        } else {
+            const int64_t at = (int64_t)blockIdx.x * kKv8MaxRows + r;
+            p.part_o[at * kDh + d] = A;
+            if (d == 0) {
+                p.part_ml[at * 2] = M;
+                p.part_ml[at * 2 + 1] = L;
+            }
+        }
     }
 }
 
-// Join of the runs that span CTAs: `wpr` warps to a row, a lane owns four of its Dh columns. The rows are
-// those of all runs (by_cta = 0) or, where there are more runs than CTAs, of the CTAs: CTA c then stands
-// for the run that begins in its range and reaches past it (there is at most one).
+// Join of the runs that were cut: `wpr` warps to a row (a query head), a lane owns four of its Dh columns.
 constexpr int kKv8MergeU = 8;  // partials in flight per lane
 
 __global__ void __launch_bounds__(1024)
-k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int by_cta, int wpr, int64_t n_rows) {
+k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int wpr) {
     extern __shared__ __align__(16) float s_join[];  // [warp][Dh + 4]: columns, m, l
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int runs_b = p.g.Hkv * p.rts;
-    const int64_t r = ((int64_t)blockIdx.x * (blockDim.x >> 5) + wp) / wpr;
+    const int r = (blockIdx.x * (blockDim.x >> 5) + wp) / wpr;  // row of out
     const int sub = wp & (wpr - 1);
-    const int row = (int)(r & (p.rows - 1));
-    int b = 0, run = 0, c = 0, ns = 0, first = 0;
-    if (r < n_rows) {
-        const int64_t x = r / p.rows;  // run or CTA
-        int64_t r0, r1;                // the run's units
-        bool mine = true;
-        if (by_cta) {
-            c = (int)x;
-            const int64_t u0 = kv8_div((int64_t)c * p.F, p.G), u1 = kv8_div(((int64_t)c + 1) * p.F, p.G);
-            b = kv8_seq_of(tab, runs_b, u1 - 1);
-            const int cost = tab.cost_off[b + 1] - tab.cost_off[b];
-            const int64_t base = (int64_t)tab.cost_off[b] * runs_b;
-            run = (int)kv8_div(u1 - 1 - base, cost);
-            r0 = base + (int64_t)run * cost;
-            r1 = r0 + cost;
-            mine = u1 > u0 && r0 >= u0 && r1 > u1;
-        } else {
-            b = (int)x / runs_b;
-            run = (int)x - b * runs_b;
-            const int cost = tab.cost_off[b + 1] - tab.cost_off[b];
-            r0 = (int64_t)tab.cost_off[b] * runs_b + (int64_t)run * cost;
-            r1 = r0 + cost;
-            c = kv8_cta_of(r0, p.F, p.G);
-        }
-        if (mine) {
-            ns = kv8_cta_of(r1 - 1, p.F, p.G) - c + 1;
-            first = r0 > kv8_div((int64_t)c * p.F, p.G) ? 1 : 0;
-        }
+    const int b = r / p.H, run = (r - b * p.H) / p.rows, row = r & (p.rows - 1);
+    int parts = 0, cta = 0;
+    if (b < tab.B) {
+        parts = (tab.cta_off[b + 1] - tab.cta_off[b]) >> p.runs_log2;
+        cta = tab.cta_off[b] + run;
     }
     pdl_wait();
-    // ns == 1: written by the CTA that held the run
+    // parts == 1: written by the CTA that held the run
     float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ns > 1) {
-        for (int i0 = sub; i0 < ns; i0 += wpr * kKv8MergeU) {
+    if (parts > 1) {
+        for (int i0 = sub; i0 < parts; i0 += wpr * kKv8MergeU) {
             float4 v[kKv8MergeU];
             float2 ml[kKv8MergeU];
 #pragma unroll
@@ -620,8 +564,8 @@ k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int by_cta, int wpr, i
                 const int i = i0 + k * wpr;
                 v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                 ml[k] = make_float2(-INFINITY, 0.f);
-                if (i < ns) {
-                    const int64_t at = (2 * (int64_t)(c + i) + (i == 0 ? first : 0)) * kKv8MaxRows + row;
+                if (i < parts) {
+                    const int64_t at = (int64_t)(cta + (i << p.runs_log2)) * kKv8MaxRows + row;
                     v[k] = *reinterpret_cast<const float4*>(p.part_o + at * kDh + lane * 4);
                     ml[k] = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
                 }
@@ -668,12 +612,10 @@ k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int by_cta, int wpr, i
             a.z = fmaf(w, v.z, a.z); a.w = fmaf(w, v.w, a.w);
         }
     }
-    if (ns > 1) {
-        const int h = run / p.rts, rt = run - h * p.rts;
-        const int q = b * p.H + (h * p.rts + rt) * p.rows + row;
+    if (parts > 1) {
         const float4 y = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x / l, a.y / l, a.z / l, a.w / l);
-        *reinterpret_cast<float4*>(p.out + (int64_t)q * kDh + lane * 4) = y;
-        if (lane == 0 && p.lse != nullptr) p.lse[q] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        *reinterpret_cast<float4*>(p.out + (int64_t)r * kDh + lane * 4) = y;
+        if (lane == 0 && p.lse != nullptr) p.lse[r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
 }
 
@@ -685,56 +627,70 @@ static cudaError_t kv8_set_attrs(int* least) {
     int n = 0;
     const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_kv8_attn<SETS, PLO, WARPS>, WARPS * 32,
                                                                         kv8_smem(SETS, WARPS));
-    if (n < *least) *least = n;
+    if (n * WARPS < *least) *least = n * WARPS;
     return f;
 }
 
-// Kernel attributes; the CTAs (of kKv8Warps) that the device holds at once, whichever variant runs.
-cudaError_t kv8_init_attrs(int num_sms, int* ctas) {
-    int n = 16, wide = 16;
-    cudaError_t e = kv8_set_attrs<1, false, kKv8Warps>(&n);
-    if (e == cudaSuccess) e = kv8_set_attrs<1, true, kKv8Warps>(&n);
-    if (e == cudaSuccess) e = kv8_set_attrs<3, false, kKv8Warps>(&n);
-    if (e == cudaSuccess) e = kv8_set_attrs<3, true, kKv8Warps>(&n);
-    if (e == cudaSuccess) e = kv8_set_attrs<1, false, kKv8WideWarps>(&wide);
-    if (e == cudaSuccess) e = kv8_set_attrs<1, true, kKv8WideWarps>(&wide);
-    if (e == cudaSuccess) e = kv8_set_attrs<3, false, kKv8WideWarps>(&wide);
-    if (e == cudaSuccess) e = kv8_set_attrs<3, true, kKv8WideWarps>(&wide);
-    if (e == cudaSuccess && (n < 1 || wide < 1)) e = cudaErrorLaunchOutOfResources;
-    *ctas = n * num_sms;
+template <int WARPS>
+static cudaError_t kv8_set_all(int* least) {
+    cudaError_t e = kv8_set_attrs<1, false, WARPS>(least);
+    if (e == cudaSuccess) e = kv8_set_attrs<1, true, WARPS>(least);
+    if (e == cudaSuccess) e = kv8_set_attrs<3, false, WARPS>(least);
+    if (e == cudaSuccess) e = kv8_set_attrs<3, true, WARPS>(least);
     return e;
 }
 
-size_t kv8_part_o_bytes(int ctas) { return (size_t)2 * ctas * kKv8MaxRows * kDh * 4; }
-size_t kv8_part_ml_bytes(int ctas) { return (size_t)2 * ctas * kKv8MaxRows * 2 * 4; }
-
-// Whether some run spans two CTAs of the even split.
-static bool kv8_splits(const Kv8Tab& tab, int runs_b, int64_t F, int G) {
-    int b = 0;
-    for (int c = 1; c < G; ++c) {
-        const int64_t u = (int64_t)c * F / G;
-        while (u >= (int64_t)tab.cost_off[b + 1] * runs_b) ++b;
-        if ((u - (int64_t)tab.cost_off[b] * runs_b) % (tab.cost_off[b + 1] - tab.cost_off[b]) != 0) return true;
-    }
-    return false;
+// Kernel attributes; every variant has to reach 16 warps an SM, which the plan counts on.
+cudaError_t kv8_init_attrs() {
+    int least = 16;
+    cudaError_t e = kv8_set_all<4>(&least);
+    if (e == cudaSuccess) e = kv8_set_all<8>(&least);
+    if (e == cudaSuccess) e = kv8_set_all<16>(&least);
+    return e == cudaSuccess && least < 16 ? cudaErrorLaunchOutOfResources : e;
 }
 
-template <int SETS>
-static cudaError_t kv8_launch(cudaLaunchConfig_t& cfg, const Kv8AttnParams& p, const Kv8Tab& kt, uint32_t* err) {
-    const int warps = p.by_run ? kKv8WideWarps : kKv8Warps;
-    const bool plo = p.rows > 4;
+// Most CTAs that a call with cut runs launches: four of four warps an SM.
+static int kv8_max_ctas(int num_sms) { return 4 * num_sms; }
+size_t kv8_part_o_bytes(int num_sms) { return (size_t)kv8_max_ctas(num_sms) * kKv8MaxRows * kDh * 4; }
+size_t kv8_part_ml_bytes(int num_sms) { return (size_t)kv8_max_ctas(num_sms) * kKv8MaxRows * 2 * 4; }
+
+// Tiles of sequence b's runs.
+static int kv8_tiles(const Kv8Tab& t, int b, int c_log2) {
+    return (int)((((int64_t)(t.kept_off[b + 1] - t.kept_off[b]) << c_log2) + kKv8Tile - 1) / kKv8Tile);
+}
+
+// The least tiles per CTA (at least `least`) with which all runs' parts are `slots` CTAs or fewer; if there
+// are more runs than that, what leaves every run whole. `all`: the tiles of all runs, `most` of the longest.
+static int kv8_part_tiles(const Kv8Tab& t, int c_log2, int64_t runs_b, int64_t slots, int least, int most,
+                          int64_t all) {
+    const int64_t runs = runs_b * t.B;
+    if (runs >= slots || most <= least) return most > least ? most : least;
+    // the parts are at least all / T and less than all / T + runs
+    int64_t lo = (all + slots - 1) / slots, hi = (all + slots - runs - 1) / (slots - runs);
+    lo = lo < least ? least : lo;
+    hi = hi > most ? most : hi;
+    while (lo < hi) {
+        const int mid = (int)(lo + (hi - lo) / 2);
+        int64_t n = 0;
+        for (int b = 0; b < t.B; ++b) n += runs_b * ((kv8_tiles(t, b, c_log2) + mid - 1) / mid);
+        if (n <= slots) hi = mid; else lo = mid + 1;
+    }
+    return (int)lo;
+}
+
+template <int SETS, bool PLO>
+static cudaError_t kv8_launch(cudaLaunchConfig_t& cfg, int warps, const Kv8AttnParams& p, const Kv8Tab& kt,
+                              uint32_t* err) {
     cfg.blockDim = dim3(warps * 32, 1, 1);
     cfg.dynamicSmemBytes = kv8_smem(SETS, warps);
-    if (p.by_run)
-        return plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, true, kKv8WideWarps>, p, kt, err)
-                   : cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, false, kKv8WideWarps>, p, kt, err);
-    return plo ? cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, true, kKv8Warps>, p, kt, err)
-               : cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, false, kKv8Warps>, p, kt, err);
+    return warps == 4   ? cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, PLO, 4>, p, kt, err)
+           : warps == 8 ? cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, PLO, 8>, p, kt, err)
+                        : cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, PLO, 16>, p, kt, err);
 }
 
 // `tab`: the kept chunks of each sequence, or all of them where ids is null.
 cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv8_cache& cache, const Kv8Geom& g,
-                            int num_sms, int max_ctas, const void* q, const int32_t* ids, const int32_t* counts,
+                            int num_sms, const void* q, const int32_t* ids, const int32_t* counts,
                             const int32_t* seq_len, int len_add, float* part_o, float* part_ml, float* out,
                             float* lse, uint32_t* err, cudaStream_t stream, bool pdl) {
     Kv8AttnParams p = {};
@@ -755,36 +711,40 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     const int group = d.H / g.Hkv;
     p.rows = group < kKv8MaxRows ? group : kKv8MaxRows;
     p.rts = group / p.rows;
+    const int runs_b = g.Hkv * p.rts;
+    while ((1 << p.runs_log2) < runs_b) ++p.runs_log2;
     p.len_add = len_add;
     p.qscale = 1.4426950408889634f / sqrtf((float)kDh);
 
     Kv8Tab kt;
     kt.B = tab.B;
-    int64_t cost = 0;
-    int most = 0;  // tiles of the longest run
     for (int b = 0; b <= tab.B; ++b) {
         kt.chunk_off[b] = tab.chunk_off[b];
         kt.kept_off[b] = tab.kept_off[b];
-        kt.cost_off[b] = (int32_t)cost;
-        if (b == tab.B) break;
-        const int64_t tokens = (int64_t)(tab.kept_off[b + 1] - tab.kept_off[b]) << g.c_log2;
-        const int tiles = (int)((tokens + kKv8Tile - 1) / kKv8Tile);
-        most = tiles > most ? tiles : most;
-        cost += tiles + kKv8RunCost;
     }
-    const int runs_b = g.Hkv * p.rts;
-    const int64_t runs = (int64_t)runs_b * tab.B;
-    p.F = cost * runs_b;
-    // Short runs, few enough for one wide CTA an SM: a CTA to a run, and nothing is left to join. Else
-    // every resident CTA an equal share, but no less than a tile to a warp.
-    const bool by_run = runs <= num_sms && most <= kKv8WideTiles;
-    p.by_run = by_run;
-    int64_t G = runs;
-    if (!by_run) {
-        G = (p.F + kKv8Warps - 1) / kKv8Warps;
-        if (G > max_ctas) G = max_ctas;
+    int most = 0;  // tiles of the longest run
+    int64_t all = 0;
+    for (int b = 0; b < tab.B; ++b) {
+        const int n = kv8_tiles(kt, b, g.c_log2);
+        most = n > most ? n : most;
+        all += (int64_t)n * runs_b;
     }
-    p.G = (int)G;
+    // 16 warps to an SM, as CTAs of 16, 8 or 4. Few wide CTAs leave the least to join, but cut the work in
+    // lumps: the widest is taken whose fullest SM has at most 1.2 times its share.
+    int warps = 16, per = 0;
+    for (; warps >= 4; warps >>= 1) {
+        per = kv8_part_tiles(kt, g.c_log2, runs_b, (int64_t)num_sms * (16 / warps), 2 * warps, most, all);
+        if (warps == 4 || (double)per * (16 / warps) * num_sms <= 1.2 * (double)all) break;
+    }
+    int64_t ctas = 0;
+    bool cut = false;
+    for (int b = 0; b < tab.B; ++b) {
+        const int parts = (kv8_tiles(kt, b, g.c_log2) + per - 1) / per;
+        kt.cta_off[b] = (int32_t)ctas;
+        ctas += (int64_t)parts * runs_b;
+        cut |= parts > 1;
+    }
+    kt.cta_off[tab.B] = (int32_t)ctas;
 
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -793,27 +753,29 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    cfg.gridDim = dim3(p.G, 1, 1);
-    const int sets = d.kv_dtype == LSA_BF16 ? 1 : 3;
-    cudaError_t e = sets == 1 ? kv8_launch<1>(cfg, p, kt, err) : kv8_launch<3>(cfg, p, kt, err);
-    if (e != cudaSuccess || by_run || !kv8_splits(kt, runs_b, p.F, p.G)) return e;
-    cfg.numAttrs = 1;  // the join always follows the split kernel: overlap its launch
-    // One warp to a row where a run spans few CTAs; eight, and 32 (a block), where it spans many.
-    const int by_cta = runs > p.G ? 1 : 0;
-    const int64_t span = p.G / runs;
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    const bool plo = p.rows > 4;
+    cudaError_t e = d.kv_dtype == LSA_BF16 ? (plo ? kv8_launch<1, true>(cfg, warps, p, kt, err)
+                                                  : kv8_launch<1, false>(cfg, warps, p, kt, err))
+                                           : (plo ? kv8_launch<3, true>(cfg, warps, p, kt, err)
+                                                  : kv8_launch<3, false>(cfg, warps, p, kt, err));
+    if (e != cudaSuccess || !cut) return e;
+    // One warp to a row where a run has few parts; eight, and 32 (a block), where it has many.
+    const int64_t rows = (int64_t)d.B * d.H;
+    const int64_t span = ctas / ((int64_t)runs_b * tab.B);
     const int wpr = span <= 8 ? 1 : span <= 64 ? 8 : 32;
     const int threads = wpr == 32 ? 1024 : 256;
-    const int64_t n_rows = (by_cta ? p.G : runs) * p.rows;
-    cfg.gridDim = dim3((unsigned)((n_rows * wpr * 32 + threads - 1) / threads), 1, 1);
+    cfg.numAttrs = 1;  // the join always follows the split kernel: overlap its launch
+    cfg.gridDim = dim3((unsigned)((rows * wpr * 32 + threads - 1) / threads), 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.dynamicSmemBytes = wpr == 1 ? 0 : threads / 32 * (kDh + 4) * 4;
-    return cudaLaunchKernelEx(&cfg, k_kv8_attn_merge, p, kt, by_cta, wpr, n_rows);
+    return cudaLaunchKernelEx(&cfg, k_kv8_attn_merge, p, kt, wpr);
 }
 
 // Whether the kept tokens of one head and the rows of the cache are few enough for 32-bit counts
 // (2^31 rows of K8 are 256 GiB). A lane looks up to two batches past its warp's last tile.
 bool kv8_attn_fits(const SeqTable& tab, const Kv8Geom& g) {
-    const int64_t slack = ((int64_t)tab.B * (kKv8RunCost + 1) + 2 * kKv8Batch * kKv8WideWarps) * kKv8Tile;
+    const int64_t slack = ((int64_t)tab.B + 2 * kKv8Batch * 16) * kKv8Tile;
     return ((int64_t)tab.kept_off[tab.B] << g.c_log2) + slack < (1ll << 31) &&
            ((int64_t)tab.chunk_off[tab.B] << (g.c_log2 + g.h_log2)) < (1ll << 31);
 }

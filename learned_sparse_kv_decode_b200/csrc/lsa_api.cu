@@ -31,7 +31,7 @@ cudaError_t score_init_attrs();
 cudaError_t topk_init_attrs();
 cudaError_t refresh_init_attrs();
 cudaError_t fp8_init_attrs();
-cudaError_t kv8_init_attrs(int num_sms, int* ctas);
+cudaError_t kv8_init_attrs();
 struct ShardOffsets {
     int32_t global0[kMaxB];
 };
@@ -92,14 +92,13 @@ lsa_status device_info(DeviceInfo* out) {
         di.sms = sms;
         // kernel attributes are per device: set them here, never inside a launch (graph capture)
         if (score_init_attrs() != cudaSuccess || topk_init_attrs() != cudaSuccess ||
-            refresh_init_attrs() != cudaSuccess || fp8_init_attrs() != cudaSuccess)
+            refresh_init_attrs() != cudaSuccess || fp8_init_attrs() != cudaSuccess || kv8_init_attrs() != cudaSuccess)
             return LSA_ERR_CUDA;
         if (attn_ctas_per_device(LSA_F32, sms, &di.attn_ctas[LSA_F32]) != cudaSuccess) return LSA_ERR_CUDA;
         if (attn_ctas_per_device(LSA_BF16, sms, &di.attn_ctas[LSA_BF16]) != cudaSuccess) return LSA_ERR_CUDA;
         int la_occ = 0;
         if (la_init_attrs(&la_occ) != cudaSuccess || la_occ < 1) return LSA_ERR_CUDA;
         di.la_ctas = la_occ * sms;
-        if (kv8_init_attrs(sms, &di.kv8_ctas) != cudaSuccess) return LSA_ERR_CUDA;
         di.ready = true;
     }
     *out = di;

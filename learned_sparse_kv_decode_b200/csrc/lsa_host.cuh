@@ -11,7 +11,6 @@ struct DeviceInfo {
     int sms;
     int attn_ctas[2];  // per kv dtype (LSA_F32, LSA_BF16)
     int la_ctas;       // CTAs of the lookahead-window attention
-    int kv8_ctas;      // CTAs of the 8-bit cache's attention
 };
 
 // Facts of the current device, computed once per device.
