@@ -9,18 +9,17 @@
 // therefore run on the tensor cores. They are one group of query heads wide, far from what fills a
 // tcgen05 tile, so they use the warp-level instructions, whose operands come from registers.
 //
-//  * S = q K^T takes the codes as they are (m16n8k32, e4m3). A row of q, scaled by a power of two, is
-//    split into e4m3 terms of four bits each, term i worth 16^-i: two terms hold a bf16 number, six an
-//    fp32 one. The terms lie in the rows of the 16-row operand that a group of up to 8 heads leaves
-//    free: two terms cost nothing extra, six cost three products. (The same product in f16, with a
-//    conversion per two codes, took 48 more instructions per 16 tokens.)
-//  * O^T = V^T P^T runs in f16 (m16n8k16), for the weights P need more bits than e4m3 terms would give
-//    cheaply. An e4m3 code is an f16 number exactly. P, at most 2^14, is split into f16 hi + lo: with
-//    4 heads or fewer lo takes the free half of the 8 columns, with 8 heads a second product. Weights
-//    keep 22 bits down to 2^-28 of the largest and reach down to 2^-39.
+//  * Both products run in f16 (m16n8k16) with fp32 accumulation: an e4m3 code is an f16 number exactly,
+//    and one conversion unpacks two. (The e4m3 form of the instruction is no cheaper: the compiler turns
+//    it into the same conversions and f16 products, and adds; it took 96 more instructions a tile.)
+//  * Full precision from f16 operands. A row of q, scaled by a power of two, is split into f16 hi + lo; lo
+//    lies in the eight rows of the 16-row operand that a group of up to 8 heads leaves free. The weights
+//    P, at most 2^14, are split in the same way: with 4 heads or fewer, lo takes the free half of the 8
+//    columns, with 8 heads a second product. Weights keep 22 bits down to 2^-28 of the largest and reach
+//    down to 2^-39.
 //  * The reduction index of a product may be permuted as long as both operands agree, so each lane uses
 //    whole 16-byte pieces as they come. Lane (g, t) of a warp (g = lane / 4, t = lane % 4) takes bytes
-//    32 t .. 32 t + 31 of token g's row of K; and bytes 16 g .. 16 g + 15 of tokens 2 t and 2 t + 1 of V,
+//    32 t .. 32 t + 31 of token g's row of K (four to a step of 16 dims); and bytes 16 g .. 16 g + 15 of tokens 2 t and 2 t + 1 of V,
 //    whose bytes a permute interleaves into pairs along the tokens. S leaves its scores exactly where
 //    the second product wants P, so nothing is exchanged between them.
 //  * V's scale multiplies the weight, relative to the largest scale seen (vref), which the running
@@ -50,7 +49,7 @@ constexpr int kKv8MetaBytes = 3 * 32 * 4;
 constexpr int kKv8WarpBytes = kKv8Meta + 2 * kKv8MetaBytes;
 constexpr int kKv8JoinBytes = kKv8MaxRows * (kDh + 2) * 4;  // of a warp; takes the tiles' place
 static_assert(kKv8JoinBytes <= kKv8WarpBytes, "the join's buffers lie where the tiles were");
-__host__ __device__ constexpr int kv8_smem(int sets, int warps) { return warps * kKv8WarpBytes + sets * 4 * 32 * 16; }
+__host__ __device__ constexpr int kv8_smem(int warps) { return warps * kKv8WarpBytes + 8 * 32 * 16; }
 
 // Prefix tables of one call: the kept (or all) chunks, and the CTAs (all heads' parts).
 struct Kv8Tab {
@@ -88,14 +87,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
-
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1,
-                                         const float (&c)[4]) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
@@ -140,9 +131,9 @@ __device__ __forceinline__ int kv8_seq_of(const Kv8Tab& tab, int c) {
     return lo;
 }
 
-// Grid: all parts of all runs; WARPS * 32 threads. SETS: products of S, two terms of q each (bf16: 1,
-// fp32: 3); PLO: groups of 8 (a second product for P's low halves).
-template <int SETS, bool PLO, int WARPS>
+// Grid: all parts of all runs; WARPS * 32 threads. BF16: the type of q; PLO: groups of 8 (a second product
+// for P's low halves).
+template <bool BF16, bool PLO, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -185,7 +176,7 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     const uint32_t ka0 = slot + g * kDh + ((2 * t ^ g) << 4), ka1 = ka0 ^ 16;
     const uint32_t va0 = slot + kKv8SlotV + 2 * t * kDh + ((g ^ 2 * t) << 4);
     const uint32_t va1 = slot + kKv8SlotV + (2 * t + 1) * kDh + ((g ^ (2 * t + 1)) << 4);
-    const uint32_t qs = smem_u32(smem) + WARPS * kKv8WarpBytes + lane * 16;  // q's terms: [set][step][lane]
+    const uint32_t qs = smem_u32(smem) + WARPS * kKv8WarpBytes + lane * 16;  // q's halves: [step][lane]
 
     // ---- what the lanes know of the octets being copied: lane L has octet L % 4 of tile (batch) + L / 4.
     // Its first row in the cache stays in a register; its scales and its count of tokens that take part go
@@ -261,13 +252,12 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     copy(0, p.K8, 0);
     copy(0, p.V8, kKv8SlotV);
 
-    // ---- q: row g % rows, scaled to stay below 256, as e4m3 terms worth 16^-i; each of four warps does a
-    // step's share of the 128 values (8 per lane)
+    // ---- q: row g % rows, scaled to stay below 2^15, as f16 hi + lo; each of four warps does two steps'
+    // share of the 128 values (8 per lane)
     float qmul;
     {
         const int64_t at = (int64_t)(qrow0 + (g & (p.rows - 1))) * kDh + t * 32;
         auto load = [&](int i, float* x) {  // values 8 i .. 8 i + 7 of the lane's 32
-            constexpr bool BF16 = SETS == 1;
             octet_floats<BF16>(octet_load<BF16>(p.q + at * (BF16 ? 2 : 4), i), x);
         };
         float top = 0.f;
@@ -284,11 +274,11 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // top < 2^(ex + 1): times 2^(7 - ex) it stays below 2^8. The factor is kept within fp32.
+        // top < 2^(ex + 1): times 2^(14 - ex) it stays below 2^15. The factor is kept within fp32.
         int ex = (int)(__float_as_uint(top) >> 23) - 127;
         ex = ex < -110 ? -110 : ex;
-        const float up = __uint_as_float((uint32_t)(7 - ex + 127) << 23);
-        qmul = p.qscale * __uint_as_float((uint32_t)(ex - 7 + 127) << 23);
+        const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+        qmul = p.qscale * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
         // a row with an infinity or a NaN has no finite scores
         const uint32_t bad = __ballot_sync(0xffffffffu, nan || !(top < INFINITY));
         if (bad >> (lane & 28) & 15) qmul = __uint_as_float(0x7fc00000u);
@@ -296,23 +286,16 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             float y[8];
             load(warp, y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= up;
-#pragma unroll
-            for (int k = 0; k < SETS; ++k) {
-                uint32_t a[4];  // the 16-row operand's registers: term 2 k in rows 0..7, 2 k + 1 in rows 8..15
+            for (int i = 0; i < 2; ++i) {  // the 16-row operand of step 2 warp + i: hi in rows 0..7, lo in rows 8..15
+                uint32_t a[4];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t w = e4m3x4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-                        a[2 * i + j] = w;
-                        float f[4];
-                        e4m3x4_floats(w, f);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[4 * i + e] = (y[4 * i + e] - f[e]) * 16.f;
-                    }
+                    const float x0 = y[4 * i + 2 * j] * up, x1 = y[4 * i + 2 * j + 1] * up;
+                    a[2 * j] = f16x2_rn(x0, x1);
+                    const float2 f = f16x2_floats(a[2 * j]);
+                    a[2 * j + 1] = f16x2_rn(x0 - f.x, x1 - f.y);
                 }
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (k * 4 + warp) * 512), "r"(a[0]),
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (2 * warp + i) * 512), "r"(a[0]),
                              "r"(a[1]), "r"(a[2]), "r"(a[3])
                              : "memory");
             }
@@ -347,42 +330,31 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         const bool whole = (full >> l0 & 15u) == 15u;
         const uint32_t mb = mt - 4 * lane + 4 * l0;  // of the tile's four octets
 
-        // ---- S: the terms of q against the tile's tokens
+        // ---- S: the halves of q against the tile's tokens
         float sc[8];
         {
-            constexpr int OC = SETS == 1 ? 4 : 2;  // octets at a time: what the registers hold
+            uint32_t kw[4][8];
 #pragma unroll
-            for (int i0 = 0; i0 < 4; i0 += OC) {
-                if (SETS > 1) __syncwarp();  // keeps the second half's loads from moving up
-                uint32_t kw[OC][8];
+            for (int i = 0; i < 4; ++i) {
+                const uint4 ka = kv8_lds16(ka0 + i * 8 * kDh), kb = kv8_lds16(ka1 + i * 8 * kDh);
+                kw[i][0] = ka.x; kw[i][1] = ka.y; kw[i][2] = ka.z; kw[i][3] = ka.w;
+                kw[i][4] = kb.x; kw[i][5] = kb.y; kw[i][6] = kb.z; kw[i][7] = kb.w;
+            }
+            float c[4][4];
 #pragma unroll
-                for (int i = 0; i < OC; ++i) {
-                    const uint4 ka = kv8_lds16(ka0 + (i0 + i) * 8 * kDh), kb = kv8_lds16(ka1 + (i0 + i) * 8 * kDh);
-                    kw[i][0] = ka.x; kw[i][1] = ka.y; kw[i][2] = ka.z; kw[i][3] = ka.w;
-                    kw[i][4] = kb.x; kw[i][5] = kb.y; kw[i][6] = kb.z; kw[i][7] = kb.w;
+            for (int s = 0; s < 8; ++s) {
+                const uint4 a = kv8_lds16(qs + s * 512);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t b0 = e4m3lo_f16x2(kw[i][s]), b1 = e4m3hi_f16x2(kw[i][s]);
+                    if (s == 0) mma_f16(c[i], a.x, a.y, a.z, a.w, b0, b1, zero);
+                    else mma_f16(c[i], a.x, a.y, a.z, a.w, b0, b1, c[i]);
                 }
+            }
 #pragma unroll
-                for (int k = SETS - 1; k >= 0; --k) {
-                    float c[OC][4];
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const uint4 a = kv8_lds16(qs + (k * 4 + s) * 512);
-#pragma unroll
-                        for (int i = 0; i < OC; ++i) {
-                            if (s == 0) mma_e4m3(c[i], a, kw[i][0], kw[i][1], zero);
-                            else mma_e4m3(c[i], a, kw[i][2 * s], kw[i][2 * s + 1], c[i]);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < OC; ++i) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& y = sc[2 * (i0 + i) + e];
-                            const float hi = k == SETS - 1 ? c[i][2 + e] : fmaf(y, 0.0625f, c[i][2 + e]);
-                            y = fmaf(hi, 0.0625f, c[i][e]);
-                        }
-                    }
-                }
+            for (int i = 0; i < 4; ++i) {
+                sc[2 * i] = c[i][0] + c[i][2];
+                sc[2 * i + 1] = c[i][1] + c[i][3];
             }
             const uint4 k4 = kv8_lds16(mb);
             const uint32_t ks[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -620,23 +592,23 @@ k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int wpr) {
 }
 
 // ------------------------------------------------------------------ host side
-template <int SETS, bool PLO, int WARPS>
+template <bool BF16, bool PLO, int WARPS>
 static cudaError_t kv8_set_attrs(int* least) {
-    const cudaError_t e = set_smem_attrs(k_kv8_attn<SETS, PLO, WARPS>, kv8_smem(SETS, WARPS));
+    const cudaError_t e = set_smem_attrs(k_kv8_attn<BF16, PLO, WARPS>, kv8_smem(WARPS));
     if (e != cudaSuccess) return e;
     int n = 0;
-    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_kv8_attn<SETS, PLO, WARPS>, WARPS * 32,
-                                                                        kv8_smem(SETS, WARPS));
+    const cudaError_t f = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_kv8_attn<BF16, PLO, WARPS>, WARPS * 32,
+                                                                        kv8_smem(WARPS));
     if (n * WARPS < *least) *least = n * WARPS;
     return f;
 }
 
 template <int WARPS>
 static cudaError_t kv8_set_all(int* least) {
-    cudaError_t e = kv8_set_attrs<1, false, WARPS>(least);
-    if (e == cudaSuccess) e = kv8_set_attrs<1, true, WARPS>(least);
-    if (e == cudaSuccess) e = kv8_set_attrs<3, false, WARPS>(least);
-    if (e == cudaSuccess) e = kv8_set_attrs<3, true, WARPS>(least);
+    cudaError_t e = kv8_set_attrs<true, false, WARPS>(least);
+    if (e == cudaSuccess) e = kv8_set_attrs<true, true, WARPS>(least);
+    if (e == cudaSuccess) e = kv8_set_attrs<false, false, WARPS>(least);
+    if (e == cudaSuccess) e = kv8_set_attrs<false, true, WARPS>(least);
     return e;
 }
 
@@ -678,14 +650,14 @@ static int kv8_part_tiles(const Kv8Tab& t, int c_log2, int64_t runs_b, int64_t s
     return (int)lo;
 }
 
-template <int SETS, bool PLO>
+template <bool BF16, bool PLO>
 static cudaError_t kv8_launch(cudaLaunchConfig_t& cfg, int warps, const Kv8AttnParams& p, const Kv8Tab& kt,
                               uint32_t* err) {
     cfg.blockDim = dim3(warps * 32, 1, 1);
-    cfg.dynamicSmemBytes = kv8_smem(SETS, warps);
-    return warps == 4   ? cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, PLO, 4>, p, kt, err)
-           : warps == 8 ? cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, PLO, 8>, p, kt, err)
-                        : cudaLaunchKernelEx(&cfg, k_kv8_attn<SETS, PLO, 16>, p, kt, err);
+    cfg.dynamicSmemBytes = kv8_smem(warps);
+    return warps == 4   ? cudaLaunchKernelEx(&cfg, k_kv8_attn<BF16, PLO, 4>, p, kt, err)
+           : warps == 8 ? cudaLaunchKernelEx(&cfg, k_kv8_attn<BF16, PLO, 8>, p, kt, err)
+                        : cudaLaunchKernelEx(&cfg, k_kv8_attn<BF16, PLO, 16>, p, kt, err);
 }
 
 // `tab`: the kept chunks of each sequence, or all of them where ids is null.
@@ -755,10 +727,10 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     cfg.numAttrs = pdl ? 1 : 0;
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     const bool plo = p.rows > 4;
-    cudaError_t e = d.kv_dtype == LSA_BF16 ? (plo ? kv8_launch<1, true>(cfg, warps, p, kt, err)
-                                                  : kv8_launch<1, false>(cfg, warps, p, kt, err))
-                                           : (plo ? kv8_launch<3, true>(cfg, warps, p, kt, err)
-                                                  : kv8_launch<3, false>(cfg, warps, p, kt, err));
+    cudaError_t e = d.kv_dtype == LSA_BF16 ? (plo ? kv8_launch<true, true>(cfg, warps, p, kt, err)
+                                                  : kv8_launch<true, false>(cfg, warps, p, kt, err))
+                                           : (plo ? kv8_launch<false, true>(cfg, warps, p, kt, err)
+                                                  : kv8_launch<false, false>(cfg, warps, p, kt, err));
     if (e != cudaSuccess || !cut) return e;
     // One warp to a row where a run has few parts; eight, and 32 (a block), where it has many.
     const int64_t rows = (int64_t)d.B * d.H;

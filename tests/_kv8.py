@@ -111,7 +111,7 @@ def attention(q, vals_k, ks, vals_v, vs, tokens):
 
 
 def attn_tolerance(A, top, n_tokens, q_err=0.0):
-    """(out, lse) bounds per head. With u = 2^-24: q as e4m3 terms is off by 2^-22 of its row's largest, a product
+    """(out, lse) bounds per head. With u = 2^-24: q as two f16 halves is off by 2^-22 of its row's largest, a product
     of 128 terms accumulated in fp32 in 8 steps, each truncating, by 2^-20 of sum |q k|; scale factors and the
     exponent's argument by 4 u of a logit's size, which A bounds too: 2^-18 A together, twice over in the weights'
     quotient. The exponential, the weights' halves and the joins: 2^-20 each at most. Sums of up to n weights or
