@@ -129,17 +129,26 @@ __device__ __forceinline__ uint32_t bf16x2_rn(float lo, float hi) {
     return r;
 }
 
-// Eight floats rounded to the row's type and stored at octet o.
+// Eight floats rounded to the row's type.
+template <bool BF16>
+__device__ __forceinline__ OctetRaw<BF16> octet_pack(const float* x) {
+    OctetRaw<BF16> r;
+    if constexpr (BF16) {
+        r.v = make_uint4(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]), bf16x2_rn(x[4], x[5]), bf16x2_rn(x[6], x[7]));
+    } else {
+        r.v = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        r.w = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+    }
+    return r;
+}
+
+// The same, stored at octet o.
 template <bool BF16>
 __device__ __forceinline__ void octet_store(void* row, int o, const float* x) {
     uint8_t* p = static_cast<uint8_t*>(row) + o * (BF16 ? 16 : 32);
-    if constexpr (BF16) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]),
-                                                  bf16x2_rn(x[4], x[5]), bf16x2_rn(x[6], x[7]));
-    } else {
-        reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
+    const OctetRaw<BF16> r = octet_pack<BF16>(x);
+    reinterpret_cast<uint4*>(p)[0] = r.v;
+    if constexpr (!BF16) reinterpret_cast<uint4*>(p)[1] = r.w;
 }
 
 // Cosine and sine of position * f: the product and its reduction to a turn in 64 bits (positions of a

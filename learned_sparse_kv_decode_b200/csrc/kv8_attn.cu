@@ -650,6 +650,23 @@ static int kv8_part_tiles(const Kv8Tab& t, int c_log2, int64_t runs_b, int64_t s
     return (int)lo;
 }
 
+// Microseconds that the runs take in parts of `per` tiles, `slots` CTAs at a time: the larger of what the
+// fullest SM computes (0.2 a tile while its 16 warps have one each, 0.137 from then on) and what memory reads
+// (8 KB a tile at 7 TB/s), 3.3 for a round of CTAs to start and to join its warps, 2 where runs are left to be
+// joined and 0.8 for the host to launch that. Measured: 8 runs of 8 tiles 4.9 us as 8 CTAs of 16 warps; of 16 tiles 6.6 so, of 32 tiles 6.2 as 64
+// CTAs of 4 warps; 128 runs of 16 tiles 7.3 as 128 wide CTAs, 8.3 as 256 of 4 warps.
+static double kv8_estimate(const Kv8Tab& t, int c_log2, int64_t runs_b, int per, int64_t all, int num_sms,
+                           int64_t slots) {
+    int64_t ctas = 0;
+    for (int b = 0; b < t.B; ++b) ctas += runs_b * ((kv8_tiles(t, b, c_log2) + per - 1) / per);
+    const int64_t share = (all + num_sms - 1) / num_sms;
+    const int64_t load = ctas > slots ? (share > per ? share : per) : per * ((ctas + num_sms - 1) / num_sms);
+    const double compute = load < 16 ? 0.2 * (double)load : 1. + 0.137 * (double)load;
+    const double memory = 0.00117 * (double)all;
+    return (compute > memory ? compute : memory) + 3.3 * (double)((ctas + slots - 1) / slots) +
+           (ctas > runs_b * t.B ? 2.8 : 0.);
+}
+
 template <bool BF16, bool PLO>
 static cudaError_t kv8_launch(cudaLaunchConfig_t& cfg, int warps, const Kv8AttnParams& p, const Kv8Tab& kt,
                               uint32_t* err) {
@@ -701,12 +718,20 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
         most = n > most ? n : most;
         all += (int64_t)n * runs_b;
     }
-    // 16 warps to an SM, as CTAs of 16, 8 or 4. Few wide CTAs leave the least to join, but cut the work in
-    // lumps: the widest is taken whose fullest SM has at most 1.2 times its share.
-    int warps = 16, per = 0;
-    for (; warps >= 4; warps >>= 1) {
-        per = kv8_part_tiles(kt, g.c_log2, runs_b, (int64_t)num_sms * (16 / warps), 2 * warps, most, all);
-        if (warps == 4 || (double)per * (16 / warps) * num_sms <= 1.2 * (double)all) break;
+    // 16 warps to an SM, as CTAs of 16, 8 or 4. Wide CTAs leave less to join but cut the work in lumps, and
+    // idle warps where runs are short; the form with the least estimated time is taken, the wider one where
+    // it hardly matters.
+    int warps = 0, per = 0;
+    double best = 0.;
+    for (int w = 16; w >= 4; w >>= 1) {
+        const int64_t slots = (int64_t)num_sms * (16 / w);
+        const int n = kv8_part_tiles(kt, g.c_log2, runs_b, slots, w, most, all);
+        const double t = kv8_estimate(kt, g.c_log2, runs_b, n, all, num_sms, slots);
+        if (warps == 0 || t < 0.98 * best) {
+            warps = w;
+            per = n;
+            best = t;
+        }
     }
     int64_t ctas = 0;
     bool cut = false;

@@ -57,27 +57,32 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
         float wa[8], wb[8];
         int have = -1;  // whose weights are loaded: 0 queries, 1 keys
         const int u1 = min(r.units, (slice + 1) * r.per);
+        OctetRaw<BF16> ra, rb;
+        auto load = [&](int u) {  // a unit ahead of its use, so that a warp has two in flight
+            const int part = u >= qu, h = ((part ? u - qu : u) << 2) + grp;
+            if (u < u1 && h < (part ? r.Hkv : r.H)) {
+                const uint8_t* src = (part ? r.k + tok * r.k_stride : r.q + tok * r.q_stride) + (int64_t)h * kRow;
+                ra = octet_load<BF16>(src, oa);
+                rb = octet_load<BF16>(src, ob);
+            }
+        };
+        ra = rb = OctetRaw<BF16>{};
+        load(slice * r.per);
         for (int u = slice * r.per; u < u1; ++u) {
-            const int part = u >= qu;
+            const int part = u >= qu, h = ((part ? u - qu : u) << 2) + grp;
             const float* weight = part ? pp.k_weight : pp.q_weight;
+            float x[8], y[8];
+            octet_floats<BF16>(ra, x);
+            octet_floats<BF16>(rb, y);
+            load(u + 1);
             if (part != have && weight != nullptr) {
                 load8(weight + oa * 8, wa);
                 load8(weight + ob * 8, wb);
             }
             have = part;
-            const int h = ((part ? u - qu : u) << 2) + grp;
-            const bool on = h < (part ? r.Hkv : r.H);
-            const uint8_t* src = (part ? r.k + tok * r.k_stride : r.q + tok * r.q_stride) + (int64_t)h * kRow;
-            float x[8], y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-            if (on) {
-                octet_floats<BF16>(octet_load<BF16>(src, oa), x);
-                octet_floats<BF16>(octet_load<BF16>(src, ob), y);
-            }
             if (weight != nullptr) row_norm(x, y, wa, wb, pp.eps);
             if (sub < pp.ho) row_rotate(x, y, c, s, pp.interleaved);
-            if (on) {
+            if (h < (part ? r.Hkv : r.H)) {
                 uint8_t* dst = (part ? r.ko + tok * r.ko_stride : r.qo + tok * r.qo_stride) + (int64_t)h * kRow;
                 octet_store<BF16>(dst, oa, x);
                 octet_store<BF16>(dst, ob, y);
@@ -93,6 +98,7 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
 // amax is a shuffle inside the warp (four rows) and a look at scale_block / 4 warps' words.
 constexpr int kAppendThreads = 512;
 constexpr int kAppendRows = kAppendThreads / 8;
+constexpr int kAppendCtas = 8;  // CTAs per SM that a long call is cut into
 
 struct AppendParams {
     Kv8Geom g;
@@ -157,11 +163,15 @@ __device__ __forceinline__ void rescale_codes(uint8_t* row, int sub, float ratio
     *reinterpret_cast<uint4*>(row + sub * 16) = v;
 }
 
+// Registers are what keeps loads in flight here: a bf16 row's values stay packed until they are written, a
+// head's rows are loaded while the one before it is worked on, and the angles (PREP; computed once for the
+// slice's heads) wait in shared memory, where each lane keeps its own.
 template <bool BF16, bool PREP>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, BF16 ? 2 : 1)
 k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uint32_t* err) {
     constexpr int kRow = kDh * (BF16 ? 2 : 4);
     __shared__ float s_amax[2][2][kAppendRows / 4];  // [head parity][K, V][warp]
+    __shared__ float4 s_angle[PREP ? 4 : 1][PREP ? kAppendThreads : 1];  // cosines 0-3, 4-7, sines 0-3, 4-7
     pdl_trigger();
     const int tid = threadIdx.x, sub = tid & 7, r = tid >> 3, warp = tid >> 5;
     const int slice = blockIdx.x % ap.slices;
@@ -189,61 +199,81 @@ k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uin
         const bool older = touched && pos < start;
         const bool has_old = touched && blk0 < start;
         const int64_t row_in = (int64_t)b * ap.n_new + (pos - start);
-        const int64_t chunk = tab.chunk_off[b] + (pos >> ap.g.c_log2);
+        const int h0 = slice * ap.per, h1 = min(ap.g.Hkv, h0 + ap.per);
+        // this row's place in the cache, of head h0: element offset and scale index (a head on: + C rows, + spc)
+        const int64_t ch0 = (tab.chunk_off[b] + (pos >> ap.g.c_log2)) * ap.g.Hkv + h0;
         const int within = (int)(pos & ((1 << ap.g.c_log2) - 1));
         const bool writer = touched && r % (1 << ap.g.sb_log2) == 0 && sub == 0;
 
         int oa, ob;
         row_octets(sub, PREP ? pp.ho : 0, PREP ? pp.interleaved : 0, &oa, &ob);
-        float c[PREP ? 8 : 1], s[PREP ? 8 : 1];
-        float wa[PREP ? 8 : 1], wb[PREP ? 8 : 1];
+        const uint8_t* kr = ap.k + row_in * ap.k_stride + (int64_t)h0 * kRow;
+        const uint8_t* vr = ap.v + row_in * ap.v_stride + (int64_t)h0 * kRow;
+        OctetRaw<BF16> nka{}, nkb{}, nva{}, nvb{};
+        auto load = [&]() {
+            if (fresh) {
+                nka = octet_load<BF16>(kr, oa);
+                nkb = octet_load<BF16>(kr, ob);
+                nva = octet_load<BF16>(vr, 2 * sub);
+                nvb = octet_load<BF16>(vr, 2 * sub + 1);
+            }
+            kr += kRow;
+            vr += kRow;
+        };
+        load();
         if constexpr (PREP) {
             if (fresh && sub < pp.ho) {
+                float c[8], s[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) angle_cs((int32_t)pos, pp.inv_freq[sub * 8 + e], &c[e], &s[e]);
-            }
-            if (pp.k_weight != nullptr) {
-                load8(pp.k_weight + oa * 8, wa);
-                load8(pp.k_weight + ob * 8, wb);
+                s_angle[0][tid] = make_float4(c[0], c[1], c[2], c[3]);
+                s_angle[1][tid] = make_float4(c[4], c[5], c[6], c[7]);
+                s_angle[2][tid] = make_float4(s[0], s[1], s[2], s[3]);
+                s_angle[3][tid] = make_float4(s[4], s[5], s[6], s[7]);
             }
         }
-        const int h1 = min(ap.g.Hkv, (slice + 1) * ap.per);
-        for (int h = slice * ap.per; h < h1; ++h) {
-            float kx[8], ky[8], vx[8], vy[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) kx[e] = ky[e] = vx[e] = vy[e] = 0.f;
-            if (fresh) {
-                const uint8_t* kr = ap.k + row_in * ap.k_stride + (int64_t)h * kRow;
-                const uint8_t* vr = ap.v + row_in * ap.v_stride + (int64_t)h * kRow;
-                octet_floats<BF16>(octet_load<BF16>(kr, oa), kx);
-                octet_floats<BF16>(octet_load<BF16>(kr, ob), ky);
-                octet_floats<BF16>(octet_load<BF16>(vr, 2 * sub), vx);
-                octet_floats<BF16>(octet_load<BF16>(vr, 2 * sub + 1), vy);
-            }
+        for (int h = h0; h < h1; ++h) {
+            OctetRaw<BF16> ka = nka, kb = nkb;
+            const OctetRaw<BF16> va = nva, vb = nvb;
+            if (h + 1 < h1) load();
             // the block's scales so far (read before the barrier, written after it)
-            const int64_t ch = chunk * ap.g.Hkv + h;
+            const int64_t ch = ch0 + (h - h0);
             const int64_t si = ch * ap.g.spc + (within >> ap.g.sb_log2);
             float was_k = 0.f, was_v = 0.f;
             if (has_old) {
                 was_k = ap.k_scale[si];
                 was_v = ap.v_scale[si];
             }
-            if constexpr (PREP) {
-                if (pp.k_weight != nullptr) row_norm(kx, ky, wa, wb, pp.eps);
-                if (fresh && sub < pp.ho) row_rotate(kx, ky, c, s, pp.interleaved);
-                if constexpr (BF16) {  // what lsa_qk_norm_rope would have stored
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const uint32_t p = bf16x2_rn(kx[e], kx[e + 1]), q = bf16x2_rn(ky[e], ky[e + 1]);
-                        kx[e] = bf16lo(p);
-                        kx[e + 1] = bf16hi(p);
-                        ky[e] = bf16lo(q);
-                        ky[e + 1] = bf16hi(q);
-                    }
-                }
-            }
             bool bad = false;
-            float ak = amax16(kx, ky, &bad), av = amax16(vx, vy, &bad);
+            float ak, av;
+            {
+                float x[8], y[8];
+                octet_floats<BF16>(ka, x);
+                octet_floats<BF16>(kb, y);
+                if constexpr (PREP) {
+                    if (pp.k_weight != nullptr) {
+                        float wa[8], wb[8];
+                        load8(pp.k_weight + oa * 8, wa);
+                        load8(pp.k_weight + ob * 8, wb);
+                        row_norm(x, y, wa, wb, pp.eps);
+                    }
+                    if (fresh && sub < pp.ho) {
+                        const float4 c0 = s_angle[0][tid], c1 = s_angle[1][tid], s0 = s_angle[2][tid], s1 = s_angle[3][tid];
+                        const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                        const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                        row_rotate(x, y, c, s, pp.interleaved);
+                    }
+                    // what lsa_qk_norm_rope would have stored
+                    ka = octet_pack<BF16>(x);
+                    kb = octet_pack<BF16>(y);
+                    octet_floats<BF16>(ka, x);
+                    octet_floats<BF16>(kb, y);
+                }
+                ak = amax16(x, y, &bad);
+                octet_floats<BF16>(va, x);
+                octet_floats<BF16>(vb, y);
+                av = amax16(x, y, &bad);
+            }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
@@ -265,8 +295,13 @@ k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uin
                 uint8_t* kd = ap.K8 + ((ch << ap.g.c_log2) + within) * kDh;
                 uint8_t* vd = ap.V8 + ((ch << ap.g.c_log2) + within) * kDh;
                 if (fresh) {
-                    store_codes(kd, oa, ob, kx, ky, sk);
-                    store_codes(vd, 2 * sub, 2 * sub + 1, vx, vy, sv);
+                    float x[8], y[8];
+                    octet_floats<BF16>(ka, x);
+                    octet_floats<BF16>(kb, y);
+                    store_codes(kd, oa, ob, x, y, sk);
+                    octet_floats<BF16>(va, x);
+                    octet_floats<BF16>(vb, y);
+                    store_codes(vd, 2 * sub, 2 * sub + 1, x, y, sv);
                 } else if (older) {
                     if (sk > was_k) rescale_codes(kd, sub, was_k / sk);
                     if (sv > was_v) rescale_codes(vd, sub, was_v / sv);
@@ -357,14 +392,12 @@ cudaError_t launch_kv8_append(const lsa_dims& d, const SeqTable& tab, const lsa_
     ap.n_new = n_new;
     // a run of n tokens touches at most (n + 62) / 64 + 1 aligned windows (one token: one)
     ap.windows = (int)(((int64_t)n_new + 62) / 64 + 1);
-    ap.per = 1;
-    if (prep != nullptr) {  // the angles are computed once for a slice's heads: long slices while CTAs abound
-        const int64_t cells = (int64_t)ap.windows * d.B;
-        const int64_t want = (int64_t)num_sms * 8;
-        int64_t slices = cells >= want ? 1 : (want + cells - 1) / cells;
-        if (slices > g.Hkv) slices = g.Hkv;
-        ap.per = (int)((g.Hkv + slices - 1) / slices);
-    }
+    // Long slices while there are CTAs enough: the angles are computed once for a slice's heads, and a head's
+    // rows are loaded during the one before.
+    const int64_t cells = (int64_t)ap.windows * d.B, want = (int64_t)num_sms * kAppendCtas;
+    int64_t slices = cells >= want ? 1 : (want + cells - 1) / cells;
+    if (slices > g.Hkv) slices = g.Hkv;
+    ap.per = (int)((g.Hkv + slices - 1) / slices);
     ap.slices = (g.Hkv + ap.per - 1) / ap.per;
     const int64_t ctas = (int64_t)ap.windows * d.B * ap.slices;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;

@@ -12,7 +12,7 @@ import os
 import torch
 
 from . import abi
-from .abi import LSA_BF16, LSA_HEAD_DIM, _check, _stream, lib
+from .abi import LSA_BF16, LSA_HEAD_DIM, _check, lib
 
 HEADER = os.path.join(os.path.dirname(abi.HEADER), "lsa_kv8.h")
 
@@ -92,13 +92,17 @@ def _rows(t, name, dtype, rows, heads, device):
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) < 3 or shape[-1] != LSA_HEAD_DIM or shape[-2] != heads or t.numel() != rows * heads * LSA_HEAD_DIM:
+    shape, row = t.shape, heads * LSA_HEAD_DIM
+    if len(shape) < 3 or shape[-1] != LSA_HEAD_DIM or shape[-2] != heads or t.numel() != rows * row:
         raise ValueError(f"{name}: expected {rows} rows of [{heads}][{LSA_HEAD_DIM}], got {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    stride = t.stride()
     if stride[-1] != 1 or (heads > 1 and stride[-2] != LSA_HEAD_DIM):
         raise ValueError(f"{name}: the values of a row must lie side by side")
-    step, span = heads * LSA_HEAD_DIM, 1
-    for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+    step, span = row, 1
+    for i in range(len(shape) - 3, -1, -1):
+        n, s = shape[i], stride[i]
         if n == 1:
             continue
         if span == 1:
@@ -107,6 +111,17 @@ def _rows(t, name, dtype, rows, heads, device):
             raise ValueError(f"{name}: the rows must be evenly spaced")
         span *= n
     return t.data_ptr(), step
+
+
+# The current stream's handle without building a Stream object (a third of a small call's time), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _stream(stream, device):
+    if stream is None:
+        return _raw_stream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _device(t):
@@ -221,7 +236,7 @@ def lsa_qk_norm_rope(dims, prep, positions, q, k, q_out, k_out, stream=None) -> 
         kp, ks = _rows(k, "k", s.dtype, n, hkv, d)
         ko, kos = _rows(k_out, "k_out", s.dtype, n, hkv, d)
     _check(lib.lsa_qk_norm_rope(dims.ptr, hkv or 1, prep.check(d), n, _ptr(positions, "positions", torch.int32, n, d),
-                                qp, qs or 0, kp, ks or 0, qo, qos or 0, ko, kos or 0, _stream(stream)),
+                                qp, qs or 0, kp, ks or 0, qo, qos or 0, ko, kos or 0, _stream(stream, d)),
            "lsa_qk_norm_rope")
 
 
@@ -236,7 +251,7 @@ def lsa_kv8_append(dims, cache, prep, k, v, start, new_count, ws, stream=None) -
     wp, wn = _ws(ws, d)
     _check(lib.lsa_kv8_append(dims.ptr, cache.ptr, None if prep is None else prep.check(d), n, kp, ks, vp, vs,
                               _opt(start, "start", torch.int32, s.B, d),
-                              _opt(new_count, "new_count", torch.int32, s.B, d), wp, wn, _stream(stream)),
+                              _opt(new_count, "new_count", torch.int32, s.B, d), wp, wn, _stream(stream, d)),
            "lsa_kv8_append")
 
 
@@ -247,7 +262,7 @@ def lsa_kv8_gather(dims, cache, chunk_ids, seq_len, K_res, V_res, ws, stream=Non
     wp, wn = _ws(ws, d)
     _check(lib.lsa_kv8_gather(dims.ptr, cache.ptr, _opt(chunk_ids, "chunk_ids", torch.int32, s.kept, d),
                               _opt(seq_len, "seq_len", torch.int32, s.B, d), _ptr(K_res, "K_res", s.dtype, n, d),
-                              _ptr(V_res, "V_res", s.dtype, n, d), wp, wn, _stream(stream)), "lsa_kv8_gather")
+                              _ptr(V_res, "V_res", s.dtype, n, d), wp, wn, _stream(stream, d)), "lsa_kv8_gather")
 
 
 def lsa_kv8_decode_attn(dims, cache, q, chunk_ids, kept_count, seq_len, out, lse, ws, stream=None) -> None:
@@ -260,7 +275,7 @@ def lsa_kv8_decode_attn(dims, cache, q, chunk_ids, kept_count, seq_len, out, lse
                                    _opt(kept_count, "kept_count", torch.int32, s.B, d),
                                    _opt(seq_len, "seq_len", torch.int32, s.B, d),
                                    _ptr(out, "out", torch.float32, n * LSA_HEAD_DIM, d),
-                                   _opt(lse, "lse", torch.float32, n, d), wp, wn, _stream(stream)),
+                                   _opt(lse, "lse", torch.float32, n, d), wp, wn, _stream(stream, d)),
            "lsa_kv8_decode_attn")
 
 
@@ -284,5 +299,5 @@ def lsa_decode_step_kv8(dims, cache, prep, q_emb, chunk_emb, q, k, v, seq_len, c
                                    vp, vs or 0, _opt(seq_len, "seq_len", torch.int32, s.B, d),
                                    _ptr(chunk_ids_out, "chunk_ids_out", torch.int32, s.kept, d),
                                    _ptr(out, "out", torch.float32, n * LSA_HEAD_DIM, d),
-                                   _opt(lse, "lse", torch.float32, n, d), wp, wn, _stream(stream)),
+                                   _opt(lse, "lse", torch.float32, n, d), wp, wn, _stream(stream, d)),
            "lsa_decode_step_kv8")
