@@ -151,6 +151,12 @@ __device__ __forceinline__ void octet_store(void* row, int o, const float* x) {
     if constexpr (!BF16) reinterpret_cast<uint4*>(p)[1] = r.w;
 }
 
+__device__ __forceinline__ void load8(const float* p, float* w) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+}
+
 // Cosine and sine of position * f: the product and its reduction to a turn in 64 bits (positions of a
 // long context make angles of 2^20 rad and more, where 32 bits are off by tenths), the fraction in 32.
 __device__ __forceinline__ void angle_cs(int32_t position, float f, float* c, float* s) {
@@ -159,48 +165,82 @@ __device__ __forceinline__ void angle_cs(int32_t position, float f, float* c, fl
     sincospif((float)(2.0 * t), s, c);
 }
 
-// RMS norm of a row whose 16 values per lane are x[0..7] (octet a) and y[0..7] (octet b).
-__device__ __forceinline__ void row_norm(float* x, float* y, const float* wa, const float* wb, float eps) {
+// 1 / sqrt(mean(x^2) + eps) of a row, from its lanes' values x[0..7] (octet a) and y[0..7] (octet b).
+__device__ __forceinline__ float row_rms(const float* x, const float* y, float eps) {
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
     ss += __shfl_xor_sync(0xffffffffu, ss, 1);
     ss += __shfl_xor_sync(0xffffffffu, ss, 2);
     ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-    const float r = rsqrtf(fmaf(ss, 1.f / kDh, eps));
+    return rsqrtf(fmaf(ss, 1.f / kDh, eps));
+}
+
+// Weight and rotation are one linear map of a pair, the same for every head of a token: value v becomes
+// v a + partner b. The coefficients of a lane's 16 values (octet a, octet b), from its weights (null: 1) and
+// its eight angles, lie in shared memory as eight float4, a[16] then b[16], `stride` float4 apart; a lane
+// that is not rotated has only a.
+template <bool INTER>
+__device__ __forceinline__ void row_coefs(float4* k, int stride, const float* weight, int oa, int ob, bool rot,
+                                          const float* c, const float* s) {
+    float w[16], a[16], b[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = 1.f;
+    if (weight != nullptr) {
+        load8(weight + oa * 8, w);
+        load8(weight + ob * 8, w + 8);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        x[e] = x[e] * r * wa[e];
-        y[e] = y[e] * r * wb[e];
+        // the e-th pair: (octet a, octet b) at e, or two neighbours of one octet
+        const int p = INTER ? 2 * e : e, q = INTER ? 2 * e + 1 : 8 + e;
+        a[p] = rot ? w[p] * c[e] : w[p];
+        a[q] = rot ? w[q] * c[e] : w[q];
+        b[p] = rot ? -w[q] * s[e] : 0.f;
+        b[q] = rot ? w[p] * s[e] : 0.f;
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+        k[f * stride] = make_float4(a[4 * f], a[4 * f + 1], a[4 * f + 2], a[4 * f + 3]);
+        k[(4 + f) * stride] = make_float4(b[4 * f], b[4 * f + 1], b[4 * f + 2], b[4 * f + 3]);
     }
 }
 
-// Rotation of a lane's two octets by its eight angles.
-__device__ __forceinline__ void row_rotate(float* x, float* y, const float* c, const float* s, int interleaved) {
-    if (interleaved) {
+// A lane's values (x: octet a, y: octet b) normed by r, weighted and rotated.
+template <bool INTER>
+__device__ __forceinline__ void row_apply(float* x, float* y, float r, bool rot, const float4* k, int stride) {
+    auto pair = [r](float& u, float& v, float au, float av, float bu, float bv) {
+        const float p = u * r, q = v * r;
+        u = fmaf(p, au, q * bu);
+        v = fmaf(q, av, p * bv);
+    };
+    if (rot) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float p = x[2 * e], q = x[2 * e + 1];
-            x[2 * e] = fmaf(p, c[e], -q * s[e]);
-            x[2 * e + 1] = fmaf(q, c[e], p * s[e]);
-            const float u = y[2 * e], v = y[2 * e + 1];
-            y[2 * e] = fmaf(u, c[4 + e], -v * s[4 + e]);
-            y[2 * e + 1] = fmaf(v, c[4 + e], u * s[4 + e]);
+        for (int f = 0; f < (INTER ? 4 : 2); ++f) {
+            if constexpr (INTER) {
+                const float4 a = k[f * stride], b = k[(4 + f) * stride];
+                float* v = (f < 2 ? x : y) + 4 * (f & 1);
+                pair(v[0], v[1], a.x, a.y, b.x, b.y);
+                pair(v[2], v[3], a.z, a.w, b.z, b.w);
+            } else {
+                const float4 au = k[f * stride], av = k[(2 + f) * stride], bu = k[(4 + f) * stride], bv = k[(6 + f) * stride];
+                pair(x[4 * f], y[4 * f], au.x, av.x, bu.x, bv.x);
+                pair(x[4 * f + 1], y[4 * f + 1], au.y, av.y, bu.y, bv.y);
+                pair(x[4 * f + 2], y[4 * f + 2], au.z, av.z, bu.z, bv.z);
+                pair(x[4 * f + 3], y[4 * f + 3], au.w, av.w, bu.w, bv.w);
+            }
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float p = x[e], q = y[e];
-            x[e] = fmaf(p, c[e], -q * s[e]);
-            y[e] = fmaf(q, c[e], p * s[e]);
+        for (int f = 0; f < 4; ++f) {
+            const float4 a = k[f * stride];
+            float* v = (f < 2 ? x : y) + 4 * (f & 1);
+            v[0] = v[0] * r * a.x;
+            v[1] = v[1] * r * a.y;
+            v[2] = v[2] * r * a.z;
+            v[3] = v[3] * r * a.w;
         }
     }
-}
-
-__device__ __forceinline__ void load8(const float* p, float* w) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
 }  // namespace lsa

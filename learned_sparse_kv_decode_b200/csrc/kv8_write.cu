@@ -12,11 +12,12 @@
 namespace lsa {
 
 // ---------------------------------------------------------------- norm and rotation
-// One warp per (token, slice of heads). The token's 64 angles are computed once per warp, two to a
-// lane (the 64-bit reduction and sincospi cost as much as a dozen rows), and handed round by
-// shuffles; the warp then walks its slice four heads at a time, eight lanes to a head, so that a
-// warp's loads and stores are 1 KB runs (bf16) of the token's row.
-constexpr int kPrepThreads = 256;
+// One warp per (token, slice of heads). The token's 64 angles are computed once per warp, two to a lane
+// (the 64-bit reduction and sincospi cost as much as a row), and handed round by shuffles; weight and
+// rotation become one pair of coefficients a value, which serve all the slice's heads from shared memory
+// (in registers they would halve the warps in flight). The warp walks its slice four heads at a time, eight
+// lanes to a head: its loads and stores are 1 KB runs (bf16) of the token's row, one run ahead in flight.
+constexpr int kPrepThreads = 128;
 
 struct PrepRows {
     const uint8_t *q, *k;
@@ -25,68 +26,83 @@ struct PrepRows {
     int32_t H, Hkv;        // 0 where q or k is absent
     int64_t n_tok;
     int32_t slices;        // warps per token
-    int32_t units, per;    // four-head units per token, units per slice
+    int32_t q_per, k_per;  // four-head units per slice
 };
 
-template <bool BF16>
-__global__ void __launch_bounds__(kPrepThreads)
-k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict__ positions) {
+// Heads h0 + grp, + 4, ... below h1 of one token.
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void prep_heads(const uint8_t* src, uint8_t* dst, int h0, int h1, int grp, int oa, int ob,
+                                           bool norm, float eps, bool rot, const float4* k) {
     constexpr int kRow = kDh * (BF16 ? 2 : 4);
+    int h = h0 + grp;
+    src += (int64_t)h * kRow;
+    dst += (int64_t)h * kRow;
+    OctetRaw<BF16> ra{}, rb{};
+    if (h < h1) {
+        ra = octet_load<BF16>(src, oa);
+        rb = octet_load<BF16>(src, ob);
+    }
+    for (int u = h0; u < h1; u += 4) {  // uniform in the warp: the norm's shuffles need every lane
+        float x[8], y[8];
+        octet_floats<BF16>(ra, x);
+        octet_floats<BF16>(rb, y);
+        src += 4 * kRow;
+        if (h + 4 < h1) {
+            ra = octet_load<BF16>(src, oa);
+            rb = octet_load<BF16>(src, ob);
+        }
+        const float r = norm ? row_rms(x, y, eps) : 1.f;
+        row_apply<INTER>(x, y, r, rot, k, 8);
+        if (h < h1) {
+            octet_store<BF16>(dst, oa, x);
+            octet_store<BF16>(dst, ob, y);
+        }
+        dst += 4 * kRow;
+        h += 4;
+    }
+}
+
+template <bool BF16, bool INTER>
+__global__ void __launch_bounds__(kPrepThreads, BF16 ? 8 : 6)
+k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict__ positions) {
+    __shared__ float4 s_coef[kPrepThreads / 32][8][8];  // [warp][a, b][lane of the row]
     pdl_trigger();
     const int lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
     const int64_t w = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
-    const int64_t tok = w / r.slices;
+    const int64_t tok = r.slices == 1 ? w : w / r.slices;
     if (tok < r.n_tok) {
         const int slice = (int)(w - tok * r.slices);
-        float c[8], s[8];
+        float c2[2] = {1.f, 1.f}, s2[2] = {0.f, 0.f};
         if (pp.ho > 0) {
             const int32_t pos = positions[tok];
-            float c2[2] = {1.f, 1.f}, s2[2] = {0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 if (2 * lane + j < pp.ho * 8) angle_cs(pos, pp.inv_freq[2 * lane + j], &c2[j], &s2[j]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                c[e] = __shfl_sync(0xffffffffu, c2[e & 1], sub * 4 + (e >> 1));
-                s[e] = __shfl_sync(0xffffffffu, s2[e & 1], sub * 4 + (e >> 1));
-            }
         }
         int oa, ob;
-        row_octets(sub, pp.ho, pp.interleaved, &oa, &ob);
-        const int qu = (r.H + 3) >> 2;  // units of queries come first
-        float wa[8], wb[8];
-        int have = -1;  // whose weights are loaded: 0 queries, 1 keys
-        const int u1 = min(r.units, (slice + 1) * r.per);
-        OctetRaw<BF16> ra, rb;
-        auto load = [&](int u) {  // a unit ahead of its use, so that a warp has two in flight
-            const int part = u >= qu, h = ((part ? u - qu : u) << 2) + grp;
-            if (u < u1 && h < (part ? r.Hkv : r.H)) {
-                const uint8_t* src = (part ? r.k + tok * r.k_stride : r.q + tok * r.q_stride) + (int64_t)h * kRow;
-                ra = octet_load<BF16>(src, oa);
-                rb = octet_load<BF16>(src, ob);
-            }
-        };
-        ra = rb = OctetRaw<BF16>{};
-        load(slice * r.per);
-        for (int u = slice * r.per; u < u1; ++u) {
-            const int part = u >= qu, h = ((part ? u - qu : u) << 2) + grp;
+        row_octets(sub, pp.ho, INTER, &oa, &ob);
+        const bool rot = sub < pp.ho;
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {  // queries, keys
+            const int per = part ? r.k_per : r.q_per, n = part ? r.Hkv : r.H;
+            const int h0 = slice * per * 4, h1 = min(n, h0 + per * 4);
+            if (h0 >= h1) continue;
             const float* weight = part ? pp.k_weight : pp.q_weight;
-            float x[8], y[8];
-            octet_floats<BF16>(ra, x);
-            octet_floats<BF16>(rb, y);
-            load(u + 1);
-            if (part != have && weight != nullptr) {
-                load8(weight + oa * 8, wa);
-                load8(weight + ob * 8, wb);
+            float4* k = &s_coef[threadIdx.x >> 5][0][sub];
+            __syncwarp();  // the queries' coefficients are done with
+            {
+                float c[8], s[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    c[e] = __shfl_sync(0xffffffffu, c2[e & 1], sub * 4 + (e >> 1));
+                    s[e] = __shfl_sync(0xffffffffu, s2[e & 1], sub * 4 + (e >> 1));
+                }
+                if (grp == 0) row_coefs<INTER>(k, 8, weight, oa, ob, rot, c, s);
             }
-            have = part;
-            if (weight != nullptr) row_norm(x, y, wa, wb, pp.eps);
-            if (sub < pp.ho) row_rotate(x, y, c, s, pp.interleaved);
-            if (h < (part ? r.Hkv : r.H)) {
-                uint8_t* dst = (part ? r.ko + tok * r.ko_stride : r.qo + tok * r.qo_stride) + (int64_t)h * kRow;
-                octet_store<BF16>(dst, oa, x);
-                octet_store<BF16>(dst, ob, y);
-            }
+            __syncwarp();
+            const uint8_t* src = part ? r.k + tok * r.k_stride : r.q + tok * r.q_stride;
+            uint8_t* dst = part ? r.ko + tok * r.ko_stride : r.qo + tok * r.qo_stride;
+            prep_heads<BF16, INTER>(src, dst, h0, h1, grp, oa, ob, weight != nullptr, pp.eps, rot, k);
         }
     }
     pdl_wait();  // launched early, nothing above depends on the kernel before; the one after does
@@ -98,6 +114,7 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
 // amax is a shuffle inside the warp (four rows) and a look at scale_block / 4 warps' words.
 constexpr int kAppendThreads = 512;
 constexpr int kAppendRows = kAppendThreads / 8;
+constexpr int kAppendCoefBytes = 8 * kAppendThreads * 16;
 constexpr int kAppendCtas = 8;  // CTAs per SM that a long call is cut into
 
 struct AppendParams {
@@ -113,22 +130,22 @@ struct AppendParams {
 };
 
 // A lane's codes of one row: eight bytes at each of its octets.
-__device__ __forceinline__ void store_codes(uint8_t* row, int oa, int ob, const float* x, const float* y,
-                                            float scale) {
-    uint32_t c[4];
-    const bool p2 = (__float_as_uint(scale) & 0x807FFFFFu) == 0;
-    if (p2) {  // the usual case: multiplying by 1 / 2^e is the division, exactly
-        const float inv = 1.f / scale;
-        c[0] = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-        c[1] = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-        c[2] = e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-        c[3] = e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
-    } else {  // a block that came with another scale
-        c[0] = e4m3x4(x[0] / scale, x[1] / scale, x[2] / scale, x[3] / scale);
-        c[1] = e4m3x4(x[4] / scale, x[5] / scale, x[6] / scale, x[7] / scale);
-        c[2] = e4m3x4(y[0] / scale, y[1] / scale, y[2] / scale, y[3] / scale);
-        c[3] = e4m3x4(y[4] / scale, y[5] / scale, y[6] / scale, y[7] / scale);
+__device__ __forceinline__ void store_codes(uint8_t* row, int oa, int ob, float* x, float* y, float scale) {
+    float inv = 1.f / scale;
+    if ((__float_as_uint(scale) & 0x807FFFFFu) != 0) {  // a block that came with another scale: divide
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] /= scale;
+            y[e] /= scale;
+        }
+        inv = 1.f;
     }
+    // usually the scale is 2^e, and multiplying by 1 / 2^e is the division, exactly
+    uint32_t c[4];
+    c[0] = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    c[1] = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+    c[2] = e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    c[3] = e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
     if (ob == oa + 1) {
         *reinterpret_cast<uint4*>(row + oa * 8) = make_uint4(c[0], c[1], c[2], c[3]);
     } else {
@@ -137,17 +154,39 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int oa, int ob, const 
     }
 }
 
-// Largest finite magnitude of a lane's 16 values; sets *bad if one is not finite.
-__device__ __forceinline__ float amax16(const float* x, const float* y, bool* bad) {
-    float a = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float p = fabsf(x[e]), q = fabsf(y[e]);
-        const bool fp = p < INFINITY, fq = q < INFINITY;
-        *bad |= !(fp && fq);
-        a = fmaxf(a, fmaxf(fp ? p : 0.f, fq ? q : 0.f));
+// Magnitudes compare as integers once the sign is off, and whatever is not finite compares above the rest.
+// Bits of the largest magnitude of a lane's 16 values: as they lie in the row's type (bf16 in the low half).
+template <bool BF16>
+__device__ __forceinline__ uint32_t top_bits(const OctetRaw<BF16>& a, const OctetRaw<BF16>& b) {
+    if constexpr (BF16) {
+        const uint32_t m = 0x7FFF7FFFu;
+        const uint32_t x = __vmaxu2(__vmaxu2(a.v.x & m, a.v.y & m), __vmaxu2(a.v.z & m, a.v.w & m));
+        const uint32_t y = __vmaxu2(__vmaxu2(b.v.x & m, b.v.y & m), __vmaxu2(b.v.z & m, b.v.w & m));
+        const uint32_t z = __vmaxu2(x, y);
+        return max(z & 0xFFFFu, z >> 16);
+    } else {
+        const uint32_t m = 0x7FFFFFFFu;
+        const uint32_t x = max(max(a.v.x & m, a.v.y & m), max(a.v.z & m, a.v.w & m));
+        const uint32_t y = max(max(a.w.x & m, a.w.y & m), max(a.w.z & m, a.w.w & m));
+        const uint32_t z = max(max(b.v.x & m, b.v.y & m), max(b.v.z & m, b.v.w & m));
+        const uint32_t w = max(max(b.w.x & m, b.w.y & m), max(b.w.z & m, b.w.w & m));
+        return max(max(x, y), max(z, w));
     }
-    return a;
+}
+
+// The warp's largest finite magnitude as fp32 bits, and the error where there were others.
+template <bool BF16>
+__device__ __forceinline__ uint32_t warp_amax(const OctetRaw<BF16>& a, const OctetRaw<BF16>& b, uint32_t* err) {
+    uint32_t top = __reduce_max_sync(0xffffffffu, top_bits<BF16>(a, b));
+    if (top >= (BF16 ? 0x7F80u : 0x7F800000u)) {  // rare: look at the finite ones alone
+        if ((threadIdx.x & 31) == 0) set_error(err, kErrNonFinite);
+        float x[16], m = 0.f;
+        octet_floats<BF16>(a, x);
+        octet_floats<BF16>(b, x + 8);
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.f);
+        return __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    }
+    return BF16 ? top << 16 : top;
 }
 
 // Requantise a lane's 16 older codes of a row whose scale grows.
@@ -163,20 +202,22 @@ __device__ __forceinline__ void rescale_codes(uint8_t* row, int sub, float ratio
     *reinterpret_cast<uint4*>(row + sub * 16) = v;
 }
 
-// Registers are what keeps loads in flight here: a bf16 row's values stay packed until they are written, a
-// head's rows are loaded while the one before it is worked on, and the angles (PREP; computed once for the
-// slice's heads) wait in shared memory, where each lane keeps its own.
-template <bool BF16, bool PREP>
+// K and V go to CTAs of their own (even, odd): what a lane holds of one row is what keeps loads in flight. A
+// bf16 row's values stay packed until they are written, a head's rows are loaded while the one before it is
+// worked on, and the coefficients of weight and rotation (computed once for the slice's heads) wait in shared
+// memory, where each lane keeps its own. PREP (of K): 0 none, 1 half-split pairs, 2 interleaved pairs.
+template <bool BF16, int PREP>
 __global__ void __launch_bounds__(kAppendThreads, BF16 ? 2 : 1)
 k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uint32_t* err) {
     constexpr int kRow = kDh * (BF16 ? 2 : 4);
-    __shared__ float s_amax[2][2][kAppendRows / 4];  // [head parity][K, V][warp]
-    __shared__ float4 s_angle[PREP ? 4 : 1][PREP ? kAppendThreads : 1];  // cosines 0-3, 4-7, sines 0-3, 4-7
+    constexpr bool INTER = PREP == 2;
+    extern __shared__ float4 s_coef[];  // PREP: [8][thread]
+    __shared__ uint32_t s_amax[2][kAppendRows / 4];  // [head parity][warp], fp32 bits
     pdl_trigger();
-    const int tid = threadIdx.x, sub = tid & 7, r = tid >> 3, warp = tid >> 5;
-    const int slice = blockIdx.x % ap.slices;
-    const int win = (blockIdx.x / ap.slices) % ap.windows;
-    const int b = blockIdx.x / ap.slices / ap.windows;
+    const int tid = threadIdx.x, sub = tid & 7, r = tid >> 3, warp = tid >> 5, lane = tid & 31;
+    const bool is_v = blockIdx.x & 1;
+    const int cell = blockIdx.x >> 1;
+    const int slice = cell % ap.slices, win = cell / ap.slices % ap.windows, b = cell / ap.slices / ap.windows;
 
     const int64_t L = (int64_t)(tab.chunk_off[b + 1] - tab.chunk_off[b]) << ap.g.c_log2;
     const int64_t start = ap.start != nullptr ? ap.start[b] : 0;
@@ -198,119 +239,75 @@ k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uin
         const bool fresh = pos >= start && pos < end;
         const bool older = touched && pos < start;
         const bool has_old = touched && blk0 < start;
-        const int64_t row_in = (int64_t)b * ap.n_new + (pos - start);
-        const int h0 = slice * ap.per, h1 = min(ap.g.Hkv, h0 + ap.per);
-        // this row's place in the cache, of head h0: element offset and scale index (a head on: + C rows, + spc)
-        const int64_t ch0 = (tab.chunk_off[b] + (pos >> ap.g.c_log2)) * ap.g.Hkv + h0;
-        const int within = (int)(pos & ((1 << ap.g.c_log2) - 1));
         const bool writer = touched && r % (1 << ap.g.sb_log2) == 0 && sub == 0;
+        const int h0 = slice * ap.per, n_h = min(ap.g.Hkv - h0, ap.per);
+        const bool prep = PREP != 0 && !is_v, rot = prep && sub < pp.ho;
 
         int oa, ob;
-        row_octets(sub, PREP ? pp.ho : 0, PREP ? pp.interleaved : 0, &oa, &ob);
-        const uint8_t* kr = ap.k + row_in * ap.k_stride + (int64_t)h0 * kRow;
-        const uint8_t* vr = ap.v + row_in * ap.v_stride + (int64_t)h0 * kRow;
-        OctetRaw<BF16> nka{}, nkb{}, nva{}, nvb{};
-        auto load = [&]() {
-            if (fresh) {
-                nka = octet_load<BF16>(kr, oa);
-                nkb = octet_load<BF16>(kr, ob);
-                nva = octet_load<BF16>(vr, 2 * sub);
-                nvb = octet_load<BF16>(vr, 2 * sub + 1);
-            }
-            kr += kRow;
-            vr += kRow;
-        };
-        load();
-        if constexpr (PREP) {
-            if (fresh && sub < pp.ho) {
+        row_octets(sub, prep ? pp.ho : 0, INTER, &oa, &ob);
+        // this row of head h0 in the input and in the cache; they move on from head to head
+        const int64_t row_in = (int64_t)b * ap.n_new + (pos - start);
+        const uint8_t* src = (is_v ? ap.v + row_in * ap.v_stride : ap.k + row_in * ap.k_stride) + (int64_t)h0 * kRow;
+        const int within = (int)(pos & ((1 << ap.g.c_log2) - 1));
+        const int64_t ch0 = (tab.chunk_off[b] + (pos >> ap.g.c_log2)) * ap.g.Hkv + h0;
+        uint8_t* dst = (is_v ? ap.V8 : ap.K8) + ((ch0 << ap.g.c_log2) + within) * kDh;
+        float* scale = (is_v ? ap.v_scale : ap.k_scale) + ch0 * ap.g.spc + (within >> ap.g.sb_log2);
+
+        OctetRaw<BF16> na{}, nb{};
+        if (fresh) {
+            na = octet_load<BF16>(src, oa);
+            nb = octet_load<BF16>(src, ob);
+        }
+        if constexpr (PREP != 0) {
+            if (prep && fresh) {
                 float c[8], s[8];
+                if (rot) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) angle_cs((int32_t)pos, pp.inv_freq[sub * 8 + e], &c[e], &s[e]);
-                s_angle[0][tid] = make_float4(c[0], c[1], c[2], c[3]);
-                s_angle[1][tid] = make_float4(c[4], c[5], c[6], c[7]);
-                s_angle[2][tid] = make_float4(s[0], s[1], s[2], s[3]);
-                s_angle[3][tid] = make_float4(s[4], s[5], s[6], s[7]);
+                    for (int e = 0; e < 8; ++e) angle_cs((int32_t)pos, pp.inv_freq[sub * 8 + e], &c[e], &s[e]);
+                }
+                row_coefs<INTER>(s_coef + tid, kAppendThreads, pp.k_weight, oa, ob, rot, c, s);
             }
         }
-        for (int h = h0; h < h1; ++h) {
-            OctetRaw<BF16> ka = nka, kb = nkb;
-            const OctetRaw<BF16> va = nva, vb = nvb;
-            if (h + 1 < h1) load();
-            // the block's scales so far (read before the barrier, written after it)
-            const int64_t ch = ch0 + (h - h0);
-            const int64_t si = ch * ap.g.spc + (within >> ap.g.sb_log2);
-            float was_k = 0.f, was_v = 0.f;
-            if (has_old) {
-                was_k = ap.k_scale[si];
-                was_v = ap.v_scale[si];
+        for (int i = 0; i < n_h; ++i) {
+            OctetRaw<BF16> xa = na, xb = nb;
+            src += kRow;
+            if (fresh && i + 1 < n_h) {
+                na = octet_load<BF16>(src, oa);
+                nb = octet_load<BF16>(src, ob);
             }
-            bool bad = false;
-            float ak, av;
-            {
-                float x[8], y[8];
-                octet_floats<BF16>(ka, x);
-                octet_floats<BF16>(kb, y);
-                if constexpr (PREP) {
-                    if (pp.k_weight != nullptr) {
-                        float wa[8], wb[8];
-                        load8(pp.k_weight + oa * 8, wa);
-                        load8(pp.k_weight + ob * 8, wb);
-                        row_norm(x, y, wa, wb, pp.eps);
+            const float was = has_old ? *scale : 0.f;  // read before the barrier, written after it
+            if constexpr (PREP != 0) {
+                if (prep) {
+                    float x[8], y[8];
+                    octet_floats<BF16>(xa, x);
+                    octet_floats<BF16>(xb, y);
+                    const float rms = pp.k_weight != nullptr ? row_rms(x, y, pp.eps) : 1.f;
+                    if (fresh) {
+                        row_apply<INTER>(x, y, rms, rot, s_coef + tid, kAppendThreads);
+                        xa = octet_pack<BF16>(x);  // what lsa_qk_norm_rope would have stored
+                        xb = octet_pack<BF16>(y);
                     }
-                    if (fresh && sub < pp.ho) {
-                        const float4 c0 = s_angle[0][tid], c1 = s_angle[1][tid], s0 = s_angle[2][tid], s1 = s_angle[3][tid];
-                        const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                        const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                        row_rotate(x, y, c, s, pp.interleaved);
-                    }
-                    // what lsa_qk_norm_rope would have stored
-                    ka = octet_pack<BF16>(x);
-                    kb = octet_pack<BF16>(y);
-                    octet_floats<BF16>(ka, x);
-                    octet_floats<BF16>(kb, y);
                 }
-                ak = amax16(x, y, &bad);
-                octet_floats<BF16>(va, x);
-                octet_floats<BF16>(vb, y);
-                av = amax16(x, y, &bad);
             }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                ak = fmaxf(ak, __shfl_xor_sync(0xffffffffu, ak, o));
-                av = fmaxf(av, __shfl_xor_sync(0xffffffffu, av, o));
-            }
-            if (bad) set_error(err, kErrNonFinite);
-            if ((tid & 31) == 0) {
-                s_amax[h & 1][0][warp] = ak;
-                s_amax[h & 1][1][warp] = av;
-            }
+            uint32_t top = warp_amax<BF16>(xa, xb, err);
+            if (lane == 0) s_amax[i & 1][warp] = top;
             __syncthreads();  // the other parity's words are free again after the next one
             if (touched) {
-                const int nw = 1 << (ap.g.sb_log2 - 2), wfirst = warp & ~(nw - 1);
-                for (int i = 0; i < nw; ++i) {
-                    ak = fmaxf(ak, s_amax[h & 1][0][wfirst + i]);
-                    av = fmaxf(av, s_amax[h & 1][1][wfirst + i]);
-                }
-                const float sk = fmaxf(kv8_scale_of(ak), was_k), sv = fmaxf(kv8_scale_of(av), was_v);
-                uint8_t* kd = ap.K8 + ((ch << ap.g.c_log2) + within) * kDh;
-                uint8_t* vd = ap.V8 + ((ch << ap.g.c_log2) + within) * kDh;
+                const int nw = 1 << (ap.g.sb_log2 - 2);  // the block's warps
+                top = __reduce_max_sync(0xffffffffu, s_amax[i & 1][(warp & ~(nw - 1)) + (lane & (nw - 1))]);
+                const float sc = fmaxf(kv8_scale_of(__uint_as_float(top)), was);
                 if (fresh) {
                     float x[8], y[8];
-                    octet_floats<BF16>(ka, x);
-                    octet_floats<BF16>(kb, y);
-                    store_codes(kd, oa, ob, x, y, sk);
-                    octet_floats<BF16>(va, x);
-                    octet_floats<BF16>(vb, y);
-                    store_codes(vd, 2 * sub, 2 * sub + 1, x, y, sv);
+                    octet_floats<BF16>(xa, x);
+                    octet_floats<BF16>(xb, y);
+                    store_codes(dst, oa, ob, x, y, sc);
                 } else if (older) {
-                    if (sk > was_k) rescale_codes(kd, sub, was_k / sk);
-                    if (sv > was_v) rescale_codes(vd, sub, was_v / sv);
+                    if (sc > was) rescale_codes(dst, sub, was / sc);
                 }
-                if (writer) {
-                    ap.k_scale[si] = sk;
-                    ap.v_scale[si] = sv;
-                }
+                if (writer) *scale = sc;
             }
+            dst += (int64_t)kDh << ap.g.c_log2;
+            scale += ap.g.spc;
         }
     }
     pdl_wait();  // as in k_qk_norm_rope
@@ -347,13 +344,14 @@ cudaError_t launch_qk_norm_rope(const lsa_dims& d, int n_kv_heads, const lsa_qk_
     r.H = q != nullptr ? d.H : 0;
     r.Hkv = k != nullptr ? n_kv_heads : 0;
     r.n_tok = n_tok;
-    r.units = (r.H + 3) / 4 + (r.Hkv + 3) / 4;
     // a warp per token where there are tokens enough to fill the SMs, else the heads are split
-    const int64_t want = (int64_t)num_sms * 32;
+    const int qu = (r.H + 3) / 4, ku = (r.Hkv + 3) / 4;
+    const int64_t want = (int64_t)num_sms * 24;
     int64_t slices = n_tok >= want ? 1 : (want + n_tok - 1) / n_tok;
-    if (slices > r.units) slices = r.units;
-    r.per = (int)((r.units + slices - 1) / slices);
-    r.slices = (r.units + r.per - 1) / r.per;
+    if (slices > (qu > ku ? qu : ku)) slices = qu > ku ? qu : ku;
+    r.slices = (int)slices;
+    r.q_per = (int)((qu + slices - 1) / slices);
+    r.k_per = (int)((ku + slices - 1) / slices);
     const int64_t warps = n_tok * r.slices;
     const int64_t ctas = (warps + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
     if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -367,8 +365,11 @@ cudaError_t launch_qk_norm_rope(const lsa_dims& d, int n_kv_heads, const lsa_qk_
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(kPrepThreads, 1, 1);
     const PrepParams pp = prep_params(&prep);
-    return d.kv_dtype == LSA_BF16 ? cudaLaunchKernelEx(&cfg, k_qk_norm_rope<true>, r, pp, positions)
-                                  : cudaLaunchKernelEx(&cfg, k_qk_norm_rope<false>, r, pp, positions);
+    if (d.kv_dtype == LSA_BF16)
+        return pp.interleaved ? cudaLaunchKernelEx(&cfg, k_qk_norm_rope<true, true>, r, pp, positions)
+                              : cudaLaunchKernelEx(&cfg, k_qk_norm_rope<true, false>, r, pp, positions);
+    return pp.interleaved ? cudaLaunchKernelEx(&cfg, k_qk_norm_rope<false, true>, r, pp, positions)
+                          : cudaLaunchKernelEx(&cfg, k_qk_norm_rope<false, false>, r, pp, positions);
 }
 
 // CTAs of an append, or 0 where they pass a grid's limit.
@@ -394,12 +395,12 @@ cudaError_t launch_kv8_append(const lsa_dims& d, const SeqTable& tab, const lsa_
     ap.windows = (int)(((int64_t)n_new + 62) / 64 + 1);
     // Long slices while there are CTAs enough: the angles are computed once for a slice's heads, and a head's
     // rows are loaded during the one before.
-    const int64_t cells = (int64_t)ap.windows * d.B, want = (int64_t)num_sms * kAppendCtas;
+    const int64_t cells = (int64_t)ap.windows * d.B * 2, want = (int64_t)num_sms * kAppendCtas;
     int64_t slices = cells >= want ? 1 : (want + cells - 1) / cells;
     if (slices > g.Hkv) slices = g.Hkv;
     ap.per = (int)((g.Hkv + slices - 1) / slices);
     ap.slices = (g.Hkv + ap.per - 1) / ap.per;
-    const int64_t ctas = (int64_t)ap.windows * d.B * ap.slices;
+    const int64_t ctas = (int64_t)ap.windows * d.B * ap.slices * 2;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -411,12 +412,23 @@ cudaError_t launch_kv8_append(const lsa_dims& d, const SeqTable& tab, const lsa_
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(kAppendThreads, 1, 1);
     const PrepParams pp = prep_params(prep);
-    const bool bf = d.kv_dtype == LSA_BF16;
-    if (prep != nullptr)
-        return bf ? cudaLaunchKernelEx(&cfg, k_kv8_append<true, true>, ap, pp, tab, err)
-                  : cudaLaunchKernelEx(&cfg, k_kv8_append<false, true>, ap, pp, tab, err);
-    return bf ? cudaLaunchKernelEx(&cfg, k_kv8_append<true, false>, ap, pp, tab, err)
-              : cudaLaunchKernelEx(&cfg, k_kv8_append<false, false>, ap, pp, tab, err);
+    const int form = prep == nullptr ? 0 : prep->interleaved ? 2 : 1;
+    cfg.dynamicSmemBytes = form != 0 ? kAppendCoefBytes : 0;
+    if (d.kv_dtype == LSA_BF16)
+        return form == 0   ? cudaLaunchKernelEx(&cfg, k_kv8_append<true, 0>, ap, pp, tab, err)
+               : form == 1 ? cudaLaunchKernelEx(&cfg, k_kv8_append<true, 1>, ap, pp, tab, err)
+                           : cudaLaunchKernelEx(&cfg, k_kv8_append<true, 2>, ap, pp, tab, err);
+    return form == 0   ? cudaLaunchKernelEx(&cfg, k_kv8_append<false, 0>, ap, pp, tab, err)
+           : form == 1 ? cudaLaunchKernelEx(&cfg, k_kv8_append<false, 1>, ap, pp, tab, err)
+                       : cudaLaunchKernelEx(&cfg, k_kv8_append<false, 2>, ap, pp, tab, err);
+}
+
+cudaError_t kv8_write_init_attrs() {
+    cudaError_t e = set_smem_attrs(k_kv8_append<true, 1>, kAppendCoefBytes);
+    if (e == cudaSuccess) e = set_smem_attrs(k_kv8_append<true, 2>, kAppendCoefBytes);
+    if (e == cudaSuccess) e = set_smem_attrs(k_kv8_append<false, 1>, kAppendCoefBytes);
+    if (e == cudaSuccess) e = set_smem_attrs(k_kv8_append<false, 2>, kAppendCoefBytes);
+    return e;
 }
 
 }  // namespace lsa

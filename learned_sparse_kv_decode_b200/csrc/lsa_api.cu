@@ -32,6 +32,7 @@ cudaError_t topk_init_attrs();
 cudaError_t refresh_init_attrs();
 cudaError_t fp8_init_attrs();
 cudaError_t kv8_init_attrs();
+cudaError_t kv8_write_init_attrs();
 struct ShardOffsets {
     int32_t global0[kMaxB];
 };
@@ -92,7 +93,8 @@ lsa_status device_info(DeviceInfo* out) {
         di.sms = sms;
         // kernel attributes are per device: set them here, never inside a launch (graph capture)
         if (score_init_attrs() != cudaSuccess || topk_init_attrs() != cudaSuccess ||
-            refresh_init_attrs() != cudaSuccess || fp8_init_attrs() != cudaSuccess || kv8_init_attrs() != cudaSuccess)
+            refresh_init_attrs() != cudaSuccess || fp8_init_attrs() != cudaSuccess ||
+            kv8_init_attrs() != cudaSuccess || kv8_write_init_attrs() != cudaSuccess)
             return LSA_ERR_CUDA;
         if (attn_ctas_per_device(LSA_F32, sms, &di.attn_ctas[LSA_F32]) != cudaSuccess) return LSA_ERR_CUDA;
         if (attn_ctas_per_device(LSA_BF16, sms, &di.attn_ctas[LSA_BF16]) != cudaSuccess) return LSA_ERR_CUDA;
