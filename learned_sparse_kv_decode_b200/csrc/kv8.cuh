@@ -29,6 +29,12 @@ struct PrepParams {
     int32_t interleaved;
 };
 
+// A truth value as a type, for lambdas that are compiled for both.
+template <bool V>
+struct Const {
+    static constexpr bool value = V;
+};
+
 // ---------------------------------------------------------------- e4m3
 // Two floats -> two e4m3 (x in the low byte), to nearest even, saturating at +-448, NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
@@ -206,15 +212,22 @@ __device__ __forceinline__ void row_coefs(float4* k, int stride, const float* we
     }
 }
 
-// A lane's values (x: octet a, y: octet b) normed by r, weighted and rotated.
+// A lane's values (x: octet a, y: octet b) normed by r, weighted and rotated. `full`: every lane of the row is
+// rotated (uniform). Otherwise a lane that is not takes no part of its neighbour, not even 0 times infinity.
 template <bool INTER>
-__device__ __forceinline__ void row_apply(float* x, float* y, float r, bool rot, const float4* k, int stride) {
-    auto pair = [r](float& u, float& v, float au, float av, float bu, float bv) {
-        const float p = u * r, q = v * r;
-        u = fmaf(p, au, q * bu);
-        v = fmaf(q, av, p * bv);
-    };
-    if (rot) {
+__device__ __forceinline__ void row_apply(float* x, float* y, float r, bool rot, bool full, const float4* k,
+                                          int stride) {
+    auto apply = [&](auto all) {
+        auto pair = [&](float& u, float& v, float au, float av, float bu, float bv) {
+            const float p = u * r, q = v * r;
+            float s = q * bu, t = p * bv;
+            if constexpr (!decltype(all)::value) {
+                s = rot ? s : 0.f;
+                t = rot ? t : 0.f;
+            }
+            u = fmaf(p, au, s);
+            v = fmaf(q, av, t);
+        };
 #pragma unroll
         for (int f = 0; f < (INTER ? 4 : 2); ++f) {
             if constexpr (INTER) {
@@ -230,17 +243,8 @@ __device__ __forceinline__ void row_apply(float* x, float* y, float r, bool rot,
                 pair(x[4 * f + 3], y[4 * f + 3], au.w, av.w, bu.w, bv.w);
             }
         }
-    } else {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const float4 a = k[f * stride];
-            float* v = (f < 2 ? x : y) + 4 * (f & 1);
-            v[0] = v[0] * r * a.x;
-            v[1] = v[1] * r * a.y;
-            v[2] = v[2] * r * a.z;
-            v[3] = v[3] * r * a.w;
-        }
-    }
+    };
+    if (full) apply(Const<true>{}); else apply(Const<false>{});
 }
 
 }  // namespace lsa

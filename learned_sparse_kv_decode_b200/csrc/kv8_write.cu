@@ -32,7 +32,7 @@ struct PrepRows {
 // Heads h0 + grp, + 4, ... below h1 of one token.
 template <bool BF16, bool INTER>
 __device__ __forceinline__ void prep_heads(const uint8_t* src, uint8_t* dst, int h0, int h1, int grp, int oa, int ob,
-                                           bool norm, float eps, bool rot, const float4* k) {
+                                           bool norm, float eps, bool rot, bool full, const float4* k) {
     constexpr int kRow = kDh * (BF16 ? 2 : 4);
     int h = h0 + grp;
     src += (int64_t)h * kRow;
@@ -52,7 +52,7 @@ __device__ __forceinline__ void prep_heads(const uint8_t* src, uint8_t* dst, int
             rb = octet_load<BF16>(src, ob);
         }
         const float r = norm ? row_rms(x, y, eps) : 1.f;
-        row_apply<INTER>(x, y, r, rot, k, 8);
+        row_apply<INTER>(x, y, r, rot, full, k, 8);
         if (h < h1) {
             octet_store<BF16>(dst, oa, x);
             octet_store<BF16>(dst, ob, y);
@@ -81,29 +81,24 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
         }
         int oa, ob;
         row_octets(sub, pp.ho, INTER, &oa, &ob);
-        const bool rot = sub < pp.ho;
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {  // queries, keys
-            const int per = part ? r.k_per : r.q_per, n = part ? r.Hkv : r.H;
+        const bool rot = sub < pp.ho, full = pp.ho == 8;
+        float4* k = &s_coef[threadIdx.x >> 5][0][sub];
+        auto heads = [&](const uint8_t* src, uint8_t* dst, int n, int per, const float* weight) {
             const int h0 = slice * per * 4, h1 = min(n, h0 + per * 4);
-            if (h0 >= h1) continue;
-            const float* weight = part ? pp.k_weight : pp.q_weight;
-            float4* k = &s_coef[threadIdx.x >> 5][0][sub];
-            __syncwarp();  // the queries' coefficients are done with
-            {
-                float c[8], s[8];
+            if (h0 >= h1) return;
+            float c[8], s[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    c[e] = __shfl_sync(0xffffffffu, c2[e & 1], sub * 4 + (e >> 1));
-                    s[e] = __shfl_sync(0xffffffffu, s2[e & 1], sub * 4 + (e >> 1));
-                }
-                if (grp == 0) row_coefs<INTER>(k, 8, weight, oa, ob, rot, c, s);
+            for (int e = 0; e < 8; ++e) {
+                c[e] = __shfl_sync(0xffffffffu, c2[e & 1], sub * 4 + (e >> 1));
+                s[e] = __shfl_sync(0xffffffffu, s2[e & 1], sub * 4 + (e >> 1));
             }
+            __syncwarp();  // the queries' coefficients are done with
+            if (grp == 0) row_coefs<INTER>(k, 8, weight, oa, ob, rot, c, s);
             __syncwarp();
-            const uint8_t* src = part ? r.k + tok * r.k_stride : r.q + tok * r.q_stride;
-            uint8_t* dst = part ? r.ko + tok * r.ko_stride : r.qo + tok * r.qo_stride;
-            prep_heads<BF16, INTER>(src, dst, h0, h1, grp, oa, ob, weight != nullptr, pp.eps, rot, k);
-        }
+            prep_heads<BF16, INTER>(src, dst, h0, h1, grp, oa, ob, weight != nullptr, pp.eps, rot, full, k);
+        };
+        heads(r.q + tok * r.q_stride, r.qo + tok * r.qo_stride, r.H, r.q_per, pp.q_weight);
+        heads(r.k + tok * r.k_stride, r.ko + tok * r.ko_stride, r.Hkv, r.k_per, pp.k_weight);
     }
     pdl_wait();  // launched early, nothing above depends on the kernel before; the one after does
 }
@@ -129,23 +124,34 @@ struct AppendParams {
     int32_t slices, per;   // slices of heads per window, heads per slice
 };
 
-// A lane's codes of one row: eight bytes at each of its octets.
-__device__ __forceinline__ void store_codes(uint8_t* row, int oa, int ob, float* x, float* y, float scale) {
-    float inv = 1.f / scale;
-    if ((__float_as_uint(scale) & 0x807FFFFFu) != 0) {  // a block that came with another scale: divide
+// A lane's codes of one row: eight bytes at each of its octets. Usually the scale is 2^e, and multiplying by
+// 1 / 2^e is the division, exactly: in bf16 pairs too, as what falls below bf16's range is below e4m3's.
+template <bool BF16>
+__device__ __forceinline__ void store_codes(uint8_t* row, int oa, int ob, OctetRaw<BF16> a, OctetRaw<BF16> b,
+                                            float scale, bool power_of_two) {
+    float x[8], y[8];
+    const float inv = 1.f / scale;
+    if (BF16 && power_of_two) {
+        const uint32_t w = __float_as_uint(inv), i2 = (w & 0xFFFF0000u) | w >> 16;
+        auto mul = [i2](uint32_t& v) { asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(i2)); };
+        mul(a.v.x); mul(a.v.y); mul(a.v.z); mul(a.v.w);
+        mul(b.v.x); mul(b.v.y); mul(b.v.z); mul(b.v.w);
+        octet_floats<BF16>(a, x);
+        octet_floats<BF16>(b, y);
+    } else {
+        octet_floats<BF16>(a, x);
+        octet_floats<BF16>(b, y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            x[e] /= scale;
-            y[e] /= scale;
+            x[e] = power_of_two ? x[e] * inv : x[e] / scale;  // else: a block that came with another scale
+            y[e] = power_of_two ? y[e] * inv : y[e] / scale;
         }
-        inv = 1.f;
     }
-    // usually the scale is 2^e, and multiplying by 1 / 2^e is the division, exactly
     uint32_t c[4];
-    c[0] = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    c[1] = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-    c[2] = e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-    c[3] = e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+    c[0] = e4m3x4(x[0], x[1], x[2], x[3]);
+    c[1] = e4m3x4(x[4], x[5], x[6], x[7]);
+    c[2] = e4m3x4(y[0], y[1], y[2], y[3]);
+    c[3] = e4m3x4(y[4], y[5], y[6], y[7]);
     if (ob == oa + 1) {
         *reinterpret_cast<uint4*>(row + oa * 8) = make_uint4(c[0], c[1], c[2], c[3]);
     } else {
@@ -268,47 +274,52 @@ k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uin
                 row_coefs<INTER>(s_coef + tid, kAppendThreads, pp.k_weight, oa, ob, rot, c, s);
             }
         }
-        for (int i = 0; i < n_h; ++i) {
-            OctetRaw<BF16> xa = na, xb = nb;
-            src += kRow;
-            if (fresh && i + 1 < n_h) {
-                na = octet_load<BF16>(src, oa);
-                nb = octet_load<BF16>(src, ob);
-            }
-            const float was = has_old ? *scale : 0.f;  // read before the barrier, written after it
-            if constexpr (PREP != 0) {
-                if (prep) {
-                    float x[8], y[8];
-                    octet_floats<BF16>(xa, x);
-                    octet_floats<BF16>(xb, y);
-                    const float rms = pp.k_weight != nullptr ? row_rms(x, y, pp.eps) : 1.f;
-                    if (fresh) {
-                        row_apply<INTER>(x, y, rms, rot, s_coef + tid, kAppendThreads);
-                        xa = octet_pack<BF16>(x);  // what lsa_qk_norm_rope would have stored
-                        xb = octet_pack<BF16>(y);
+        const int nw = 1 << (ap.g.sb_log2 - 2);  // a block's warps
+        const int amax_at = (warp & ~(nw - 1)) + (lane & (nw - 1));
+        const int64_t dst_step = (int64_t)kDh << ap.g.c_log2;
+        // ALL: every row of the window is written and none of its blocks is older, as in all but a call's first
+        // and last windows.
+        auto heads = [&](auto all) {
+            constexpr bool ALL = decltype(all)::value;
+            for (int i = 0; i < n_h; ++i) {
+                OctetRaw<BF16> xa = na, xb = nb;
+                src += kRow;
+                if ((ALL || fresh) && i + 1 < n_h) {
+                    na = octet_load<BF16>(src, oa);
+                    nb = octet_load<BF16>(src, ob);
+                }
+                const float was = !ALL && has_old ? *scale : 0.f;  // read before the barrier, written after it
+                if constexpr (PREP != 0) {
+                    if (prep) {
+                        float x[8], y[8];
+                        octet_floats<BF16>(xa, x);
+                        octet_floats<BF16>(xb, y);
+                        const float rms = pp.k_weight != nullptr ? row_rms(x, y, pp.eps) : 1.f;
+                        if (ALL || fresh) {
+                            row_apply<INTER>(x, y, rms, rot, pp.ho == 8, s_coef + tid, kAppendThreads);
+                            xa = octet_pack<BF16>(x);  // what lsa_qk_norm_rope would have stored
+                            xb = octet_pack<BF16>(y);
+                        }
                     }
                 }
-            }
-            uint32_t top = warp_amax<BF16>(xa, xb, err);
-            if (lane == 0) s_amax[i & 1][warp] = top;
-            __syncthreads();  // the other parity's words are free again after the next one
-            if (touched) {
-                const int nw = 1 << (ap.g.sb_log2 - 2);  // the block's warps
-                top = __reduce_max_sync(0xffffffffu, s_amax[i & 1][(warp & ~(nw - 1)) + (lane & (nw - 1))]);
-                const float sc = fmaxf(kv8_scale_of(__uint_as_float(top)), was);
-                if (fresh) {
-                    float x[8], y[8];
-                    octet_floats<BF16>(xa, x);
-                    octet_floats<BF16>(xb, y);
-                    store_codes(dst, oa, ob, x, y, sc);
-                } else if (older) {
-                    if (sc > was) rescale_codes(dst, sub, was / sc);
+                uint32_t top = warp_amax<BF16>(xa, xb, err);
+                if (lane == 0) s_amax[i & 1][warp] = top;
+                __syncthreads();  // the other parity's words are free again after the next one
+                if (ALL || touched) {
+                    top = __reduce_max_sync(0xffffffffu, s_amax[i & 1][amax_at]);
+                    const float need = kv8_scale_of(__uint_as_float(top)), sc = ALL ? need : fmaxf(need, was);
+                    if (ALL || fresh) {
+                        store_codes<BF16>(dst, oa, ob, xa, xb, sc, ALL || (__float_as_uint(sc) & 0x807FFFFFu) == 0);
+                    } else if (older && sc > was) {
+                        rescale_codes(dst, sub, was / sc);
+                    }
+                    if (writer) *scale = sc;
                 }
-                if (writer) *scale = sc;
+                dst += dst_step;
+                scale += ap.g.spc;
             }
-            dst += (int64_t)kDh << ap.g.c_log2;
-            scale += ap.g.spc;
-        }
+        };
+        if (w0 >= start && w0 + kAppendRows <= end) heads(Const<true>{}); else heads(Const<false>{});
     }
     pdl_wait();  // as in k_qk_norm_rope
 }
