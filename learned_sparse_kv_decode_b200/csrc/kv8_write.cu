@@ -13,7 +13,7 @@ namespace lsa {
 
 // ---------------------------------------------------------------- norm and rotation
 // One warp per (token, slice of heads). The token's 64 angles are computed once per warp, two to a lane
-// (the 64-bit reduction and sincospi cost as much as a row), and handed round by shuffles; weight and
+// (a tenth of a row's work each), and handed round by shuffles; weight and
 // rotation become one pair of coefficients a value, which serve all the slice's heads from shared memory
 // (in registers they would halve the warps in flight). The warp walks its slice four heads at a time, eight
 // lanes to a head: its loads and stores are 1 KB runs (bf16) of the token's row, one run ahead in flight.
@@ -77,7 +77,7 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
             const int32_t pos = positions[tok];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (2 * lane + j < pp.ho * 8) angle_cs(pos, pp.inv_freq[2 * lane + j], &c2[j], &s2[j]);
+                if (2 * lane + j < pp.ho * 8) angle_cs<BF16>(pos, pp.inv_freq[2 * lane + j], &c2[j], &s2[j]);
         }
         int oa, ob;
         row_octets(sub, pp.ho, INTER, &oa, &ob);
@@ -208,19 +208,95 @@ __device__ __forceinline__ void rescale_codes(uint8_t* row, int sub, float ratio
     *reinterpret_cast<uint4*>(row + sub * 16) = v;
 }
 
+// What the lanes of one row know of it.
+struct AppendRow {
+    const uint8_t* src;   // the row in the input, head h0
+    uint8_t* dst;         // and in the cache
+    float* scale;         // its block's
+    int64_t dst_step;     // bytes from one head to the next in the cache
+    int32_t scale_step;
+    int32_t n_h;          // heads
+    int32_t pos;
+    bool fresh, older, has_old, touched, writer;
+};
+
+// The heads of one window. ALL: every row of it is written and none of its blocks is older, as in all but a
+// call's first and last windows. PREP: 0 none, 1 half-split pairs, 2 interleaved pairs.
+template <bool BF16, int PREP, bool ALL>
+__device__ __forceinline__ void append_heads(AppendRow w, const PrepParams& pp, int amax_at,
+                                             uint32_t (*s_amax)[kAppendRows / 4], float4* coef, uint32_t* err) {
+    constexpr int kRow = kDh * (BF16 ? 2 : 4);
+    constexpr bool INTER = PREP == 2;
+    const int sub = threadIdx.x & 7;
+    int oa, ob;
+    row_octets(sub, PREP ? pp.ho : 0, INTER, &oa, &ob);
+    OctetRaw<BF16> na{}, nb{};
+    if (ALL || w.fresh) {
+        na = octet_load<BF16>(w.src, oa);
+        nb = octet_load<BF16>(w.src, ob);
+    }
+    const bool rot = PREP != 0 && sub < pp.ho, full = PREP != 0 && pp.ho == 8, norm = PREP != 0 && pp.k_weight != nullptr;
+    const float eps = pp.eps;
+    if constexpr (PREP != 0) {
+        if (ALL || w.fresh) {
+            float c[8], s[8];
+            if (rot) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) angle_cs<BF16>(w.pos, pp.inv_freq[sub * 8 + e], &c[e], &s[e]);
+            }
+            row_coefs<INTER>(coef, kAppendThreads, pp.k_weight, oa, ob, rot, c, s);
+        }
+    }
+#pragma unroll 1
+    for (int i = 0; i < w.n_h; ++i) {
+        OctetRaw<BF16> xa = na, xb = nb;
+        w.src += kRow;
+        if ((ALL || w.fresh) && i + 1 < w.n_h) {
+            na = octet_load<BF16>(w.src, oa);
+            nb = octet_load<BF16>(w.src, ob);
+        }
+        const float was = !ALL && w.has_old ? *w.scale : 0.f;  // read before the barrier, written after it
+        if constexpr (PREP != 0) {
+            float x[8], y[8];
+            octet_floats<BF16>(xa, x);
+            octet_floats<BF16>(xb, y);
+            const float rms = norm ? row_rms(x, y, eps) : 1.f;
+            if (ALL || w.fresh) {
+                row_apply<INTER>(x, y, rms, rot, full, coef, kAppendThreads);
+                xa = octet_pack<BF16>(x);  // what lsa_qk_norm_rope would have stored
+                xb = octet_pack<BF16>(y);
+            }
+        }
+        uint32_t top = warp_amax<BF16>(xa, xb, err);
+        if ((threadIdx.x & 31) == 0) s_amax[i & 1][threadIdx.x >> 5] = top;
+        __syncthreads();  // the other parity's words are free again after the next one
+        if (ALL || w.touched) {
+            top = __reduce_max_sync(0xffffffffu, s_amax[i & 1][amax_at]);
+            const float need = kv8_scale_of(__uint_as_float(top)), sc = ALL ? need : fmaxf(need, was);
+            if (ALL || w.fresh) {
+                store_codes<BF16>(w.dst, oa, ob, xa, xb, sc, ALL || (__float_as_uint(sc) & 0x807FFFFFu) == 0);
+            } else if (w.older && sc > was) {
+                rescale_codes(w.dst, sub, was / sc);
+            }
+            if (w.writer) *w.scale = sc;
+        }
+        w.dst += w.dst_step;
+        w.scale += w.scale_step;
+    }
+}
+
 // K and V go to CTAs of their own (even, odd): what a lane holds of one row is what keeps loads in flight. A
 // bf16 row's values stay packed until they are written, a head's rows are loaded while the one before it is
 // worked on, and the coefficients of weight and rotation (computed once for the slice's heads) wait in shared
-// memory, where each lane keeps its own. PREP (of K): 0 none, 1 half-split pairs, 2 interleaved pairs.
+// memory, where each lane keeps its own. PREP is of K.
 template <bool BF16, int PREP>
 __global__ void __launch_bounds__(kAppendThreads, BF16 ? 2 : 1)
 k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uint32_t* err) {
     constexpr int kRow = kDh * (BF16 ? 2 : 4);
-    constexpr bool INTER = PREP == 2;
     extern __shared__ float4 s_coef[];  // PREP: [8][thread]
     __shared__ uint32_t s_amax[2][kAppendRows / 4];  // [head parity][warp], fp32 bits
     pdl_trigger();
-    const int tid = threadIdx.x, sub = tid & 7, r = tid >> 3, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, r = tid >> 3, warp = tid >> 5, lane = tid & 31;
     const bool is_v = blockIdx.x & 1;
     const int cell = blockIdx.x >> 1;
     const int slice = cell % ap.slices, win = cell / ap.slices % ap.windows, b = cell / ap.slices / ap.windows;
@@ -241,85 +317,33 @@ k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uin
         const int64_t blk0 = pos >> ap.g.sb_log2 << ap.g.sb_log2;  // the row's block
         const int64_t lo = blk0 > start ? blk0 : start;
         const int64_t hi = blk0 + (1 << ap.g.sb_log2) < end ? blk0 + (1 << ap.g.sb_log2) : end;
-        const bool touched = lo < hi;             // uniform in a warp: its four rows share a block
-        const bool fresh = pos >= start && pos < end;
-        const bool older = touched && pos < start;
-        const bool has_old = touched && blk0 < start;
-        const bool writer = touched && r % (1 << ap.g.sb_log2) == 0 && sub == 0;
-        const int h0 = slice * ap.per, n_h = min(ap.g.Hkv - h0, ap.per);
-        const bool prep = PREP != 0 && !is_v, rot = prep && sub < pp.ho;
-
-        int oa, ob;
-        row_octets(sub, prep ? pp.ho : 0, INTER, &oa, &ob);
-        // this row of head h0 in the input and in the cache; they move on from head to head
+        AppendRow w;
+        w.touched = lo < hi;  // uniform in a warp: its four rows share a block
+        w.fresh = pos >= start && pos < end;
+        w.older = w.touched && pos < start;
+        w.has_old = w.touched && blk0 < start;
+        w.writer = w.touched && r % (1 << ap.g.sb_log2) == 0 && (tid & 7) == 0;
+        const int h0 = slice * ap.per;
+        w.n_h = min(ap.g.Hkv - h0, ap.per);
+        w.pos = (int32_t)pos;
         const int64_t row_in = (int64_t)b * ap.n_new + (pos - start);
-        const uint8_t* src = (is_v ? ap.v + row_in * ap.v_stride : ap.k + row_in * ap.k_stride) + (int64_t)h0 * kRow;
+        w.src = (is_v ? ap.v + row_in * ap.v_stride : ap.k + row_in * ap.k_stride) + (int64_t)h0 * kRow;
         const int within = (int)(pos & ((1 << ap.g.c_log2) - 1));
         const int64_t ch0 = (tab.chunk_off[b] + (pos >> ap.g.c_log2)) * ap.g.Hkv + h0;
-        uint8_t* dst = (is_v ? ap.V8 : ap.K8) + ((ch0 << ap.g.c_log2) + within) * kDh;
-        float* scale = (is_v ? ap.v_scale : ap.k_scale) + ch0 * ap.g.spc + (within >> ap.g.sb_log2);
-
-        OctetRaw<BF16> na{}, nb{};
-        if (fresh) {
-            na = octet_load<BF16>(src, oa);
-            nb = octet_load<BF16>(src, ob);
-        }
-        if constexpr (PREP != 0) {
-            if (prep && fresh) {
-                float c[8], s[8];
-                if (rot) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) angle_cs((int32_t)pos, pp.inv_freq[sub * 8 + e], &c[e], &s[e]);
-                }
-                row_coefs<INTER>(s_coef + tid, kAppendThreads, pp.k_weight, oa, ob, rot, c, s);
-            }
-        }
+        w.dst = (is_v ? ap.V8 : ap.K8) + ((ch0 << ap.g.c_log2) + within) * kDh;
+        w.dst_step = (int64_t)kDh << ap.g.c_log2;
+        w.scale = (is_v ? ap.v_scale : ap.k_scale) + ch0 * ap.g.spc + (within >> ap.g.sb_log2);
+        w.scale_step = ap.g.spc;
         const int nw = 1 << (ap.g.sb_log2 - 2);  // a block's warps
         const int amax_at = (warp & ~(nw - 1)) + (lane & (nw - 1));
-        const int64_t dst_step = (int64_t)kDh << ap.g.c_log2;
-        // ALL: every row of the window is written and none of its blocks is older, as in all but a call's first
-        // and last windows.
-        auto heads = [&](auto all) {
-            constexpr bool ALL = decltype(all)::value;
-            for (int i = 0; i < n_h; ++i) {
-                OctetRaw<BF16> xa = na, xb = nb;
-                src += kRow;
-                if ((ALL || fresh) && i + 1 < n_h) {
-                    na = octet_load<BF16>(src, oa);
-                    nb = octet_load<BF16>(src, ob);
-                }
-                const float was = !ALL && has_old ? *scale : 0.f;  // read before the barrier, written after it
-                if constexpr (PREP != 0) {
-                    if (prep) {
-                        float x[8], y[8];
-                        octet_floats<BF16>(xa, x);
-                        octet_floats<BF16>(xb, y);
-                        const float rms = pp.k_weight != nullptr ? row_rms(x, y, pp.eps) : 1.f;
-                        if (ALL || fresh) {
-                            row_apply<INTER>(x, y, rms, rot, pp.ho == 8, s_coef + tid, kAppendThreads);
-                            xa = octet_pack<BF16>(x);  // what lsa_qk_norm_rope would have stored
-                            xb = octet_pack<BF16>(y);
-                        }
-                    }
-                }
-                uint32_t top = warp_amax<BF16>(xa, xb, err);
-                if (lane == 0) s_amax[i & 1][warp] = top;
-                __syncthreads();  // the other parity's words are free again after the next one
-                if (ALL || touched) {
-                    top = __reduce_max_sync(0xffffffffu, s_amax[i & 1][amax_at]);
-                    const float need = kv8_scale_of(__uint_as_float(top)), sc = ALL ? need : fmaxf(need, was);
-                    if (ALL || fresh) {
-                        store_codes<BF16>(dst, oa, ob, xa, xb, sc, ALL || (__float_as_uint(sc) & 0x807FFFFFu) == 0);
-                    } else if (older && sc > was) {
-                        rescale_codes(dst, sub, was / sc);
-                    }
-                    if (writer) *scale = sc;
-                }
-                dst += dst_step;
-                scale += ap.g.spc;
-            }
-        };
-        if (w0 >= start && w0 + kAppendRows <= end) heads(Const<true>{}); else heads(Const<false>{});
+        const bool all = w0 >= start && w0 + kAppendRows <= end;
+        if (PREP != 0 && !is_v) {
+            if (all) append_heads<BF16, PREP, true>(w, pp, amax_at, s_amax, s_coef + tid, err);
+            else append_heads<BF16, PREP, false>(w, pp, amax_at, s_amax, s_coef + tid, err);
+        } else {
+            if (all) append_heads<BF16, 0, true>(w, pp, amax_at, s_amax, nullptr, err);
+            else append_heads<BF16, 0, false>(w, pp, amax_at, s_amax, nullptr, err);
+        }
     }
     pdl_wait();  // as in k_qk_norm_rope
 }
