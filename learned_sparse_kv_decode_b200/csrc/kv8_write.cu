@@ -130,7 +130,7 @@ template <bool BF16>
 __device__ __forceinline__ void store_codes(uint8_t* row, int oa, int ob, OctetRaw<BF16> a, OctetRaw<BF16> b,
                                             float scale, bool power_of_two) {
     float x[8], y[8];
-    const float inv = 1.f / scale;
+    const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 2^-e of a scale 2^e
     if (BF16 && power_of_two) {
         const uint32_t w = __float_as_uint(inv), i2 = (w & 0xFFFF0000u) | w >> 16;
         auto mul = [i2](uint32_t& v) { asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(i2)); };
@@ -160,15 +160,18 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int oa, int ob, OctetR
     }
 }
 
-// Magnitudes compare as integers once the sign is off, and whatever is not finite compares above the rest.
-// Bits of the largest magnitude of a lane's 16 values: as they lie in the row's type (bf16 in the low half).
+// Bits of the largest magnitude of a lane's 16 values, as they lie in the row's type (bf16 in the low half);
+// what is not finite is above the rest. bf16 by the paired maximum of magnitudes that passes a NaN on (its
+// sign bit is then masked), fp32 as integers once the sign is off.
 template <bool BF16>
 __device__ __forceinline__ uint32_t top_bits(const OctetRaw<BF16>& a, const OctetRaw<BF16>& b) {
     if constexpr (BF16) {
-        const uint32_t m = 0x7FFF7FFFu;
-        const uint32_t x = __vmaxu2(__vmaxu2(a.v.x & m, a.v.y & m), __vmaxu2(a.v.z & m, a.v.w & m));
-        const uint32_t y = __vmaxu2(__vmaxu2(b.v.x & m, b.v.y & m), __vmaxu2(b.v.z & m, b.v.w & m));
-        const uint32_t z = __vmaxu2(x, y);
+        auto mx = [](uint32_t x, uint32_t y) {
+            uint32_t r;
+            asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+            return r;
+        };
+        const uint32_t z = mx(mx(mx(a.v.x, a.v.y), mx(a.v.z, a.v.w)), mx(mx(b.v.x, b.v.y), mx(b.v.z, b.v.w))) & 0x7FFF7FFFu;
         return max(z & 0xFFFFu, z >> 16);
     } else {
         const uint32_t m = 0x7FFFFFFFu;
@@ -231,9 +234,10 @@ __device__ __forceinline__ void append_heads(AppendRow w, const PrepParams& pp, 
     int oa, ob;
     row_octets(sub, PREP ? pp.ho : 0, INTER, &oa, &ob);
     OctetRaw<BF16> na{}, nb{};
+    const uint8_t *pa = w.src + oa * (kRow / 16), *pb = w.src + ob * (kRow / 16);
     if (ALL || w.fresh) {
-        na = octet_load<BF16>(w.src, oa);
-        nb = octet_load<BF16>(w.src, ob);
+        na = octet_load<BF16>(pa, 0);
+        nb = octet_load<BF16>(pb, 0);
     }
     const bool rot = PREP != 0 && sub < pp.ho, full = PREP != 0 && pp.ho == 8, norm = PREP != 0 && pp.k_weight != nullptr;
     const float eps = pp.eps;
@@ -250,10 +254,11 @@ __device__ __forceinline__ void append_heads(AppendRow w, const PrepParams& pp, 
 #pragma unroll 1
     for (int i = 0; i < w.n_h; ++i) {
         OctetRaw<BF16> xa = na, xb = nb;
-        w.src += kRow;
+        pa += kRow;
+        pb += kRow;
         if ((ALL || w.fresh) && i + 1 < w.n_h) {
-            na = octet_load<BF16>(w.src, oa);
-            nb = octet_load<BF16>(w.src, ob);
+            na = octet_load<BF16>(pa, 0);
+            nb = octet_load<BF16>(pb, 0);
         }
         const float was = !ALL && w.has_old ? *w.scale : 0.f;  // read before the barrier, written after it
         if constexpr (PREP != 0) {
