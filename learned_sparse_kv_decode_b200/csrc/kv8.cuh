@@ -35,6 +35,37 @@ struct Const {
     static constexpr bool value = V;
 };
 
+// ---------------------------------------------------------------- pairs of floats
+// Two floats in a register pair; one instruction works on both, each rounded as the scalar one would.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f2_floats(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // ---------------------------------------------------------------- e4m3
 // Two floats -> two e4m3 (x in the low byte), to nearest even, saturating at +-448, NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
@@ -148,11 +179,9 @@ __device__ __forceinline__ OctetRaw<BF16> octet_pack(const float* x) {
     return r;
 }
 
-// The same, stored at octet o.
 template <bool BF16>
-__device__ __forceinline__ void octet_store(void* row, int o, const float* x) {
+__device__ __forceinline__ void octet_store(void* row, int o, const OctetRaw<BF16>& r) {
     uint8_t* p = static_cast<uint8_t*>(row) + o * (BF16 ? 16 : 32);
-    const OctetRaw<BF16> r = octet_pack<BF16>(x);
     reinterpret_cast<uint4*>(p)[0] = r.v;
     if constexpr (!BF16) reinterpret_cast<uint4*>(p)[1] = r.w;
 }
@@ -180,25 +209,75 @@ __device__ __forceinline__ void angle_cs(int32_t position, float f, float* c, fl
     }
 }
 
-// 1 / sqrt(mean(x^2) + eps) of a row, from its lanes' values x[0..7] (octet a) and y[0..7] (octet b).
-__device__ __forceinline__ float row_rms(const float* x, const float* y, float eps) {
-    float ss = 0.f;
+// The 16 values of a lane as eight pairs (p, q) that a rotation mixes: p and q are the octets a and b, or
+// (INTER) the even and the odd values of both. Two pairs lie in each F2 of p and of q.
+struct RowPairs {
+    F2 p[4], q[4];
+};
+
+template <bool BF16, bool INTER>
+__device__ __forceinline__ RowPairs row_pairs(const OctetRaw<BF16>& a, const OctetRaw<BF16>& b) {
+    float x[8], y[8];
+    octet_floats<BF16>(a, x);
+    octet_floats<BF16>(b, y);
+    RowPairs r;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (INTER) {
+            const float* v = j < 2 ? x + 4 * j : y + 4 * (j - 2);
+            r.p[j] = f2(v[0], v[2]);
+            r.q[j] = f2(v[1], v[3]);
+        } else {
+            r.p[j] = f2(x[2 * j], x[2 * j + 1]);
+            r.q[j] = f2(y[2 * j], y[2 * j + 1]);
+        }
+    }
+    return r;
+}
+
+// Back to octets, rounded to the row's type.
+template <bool BF16, bool INTER>
+__device__ __forceinline__ void row_octets_of(const RowPairs& r, OctetRaw<BF16>* a, OctetRaw<BF16>* b) {
+    float x[8], y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 p = f2_floats(r.p[j]), q = f2_floats(r.q[j]);
+        if constexpr (INTER) {
+            float* v = j < 2 ? x + 4 * j : y + 4 * (j - 2);
+            v[0] = p.x; v[1] = q.x; v[2] = p.y; v[3] = q.y;
+        } else {
+            x[2 * j] = p.x; x[2 * j + 1] = p.y;
+            y[2 * j] = q.x; y[2 * j + 1] = q.y;
+        }
+    }
+    *a = octet_pack<BF16>(x);
+    *b = octet_pack<BF16>(y);
+}
+
+// 1 / sqrt(mean(x^2) + eps) of a row, from its lanes' values.
+__device__ __forceinline__ float row_rms(const RowPairs& r, float eps) {
+    F2 s = f2_mul(r.p[0], r.p[0]);
+#pragma unroll
+    for (int j = 1; j < 4; ++j) s = f2_fma(r.p[j], r.p[j], s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s = f2_fma(r.q[j], r.q[j], s);
+    const float2 h = f2_floats(s);
+    float ss = h.x + h.y;
     ss += __shfl_xor_sync(0xffffffffu, ss, 1);
     ss += __shfl_xor_sync(0xffffffffu, ss, 2);
     ss += __shfl_xor_sync(0xffffffffu, ss, 4);
     return rsqrtf(fmaf(ss, 1.f / kDh, eps));
 }
 
-// Weight and rotation are one linear map of a pair, the same for every head of a token: value v becomes
-// v a + partner b. The coefficients of a lane's 16 values (octet a, octet b), from its weights (null: 1) and
-// its eight angles, lie in shared memory as eight float4, a[16] then b[16], `stride` float4 apart; a lane
-// that is not rotated has only a.
+// Weight and rotation are one linear map of a pair, the same for every head of a token:
+//     p <- p w_p cos - q w_q sin,   q <- q w_q cos + p w_p sin.
+// The coefficients of a lane's eight pairs, from its weights (null: 1) and its eight angles, lie in shared
+// memory as eight float4, `stride` float4 apart: of p by p, of q by q, of p by q, of q by p, each two. A lane
+// that is not rotated has only the weights.
 template <bool INTER>
 __device__ __forceinline__ void row_coefs(float4* k, int stride, const float* weight, int oa, int ob, bool rot,
                                           const float* c, const float* s) {
-    float w[16], a[16], b[16];
+    float w[16], a[8][4];
 #pragma unroll
     for (int e = 0; e < 16; ++e) w[e] = 1.f;
     if (weight != nullptr) {
@@ -207,49 +286,34 @@ __device__ __forceinline__ void row_coefs(float4* k, int stride, const float* we
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        // the e-th pair: (octet a, octet b) at e, or two neighbours of one octet
-        const int p = INTER ? 2 * e : e, q = INTER ? 2 * e + 1 : 8 + e;
-        a[p] = rot ? w[p] * c[e] : w[p];
-        a[q] = rot ? w[q] * c[e] : w[q];
-        b[p] = rot ? -w[q] * s[e] : 0.f;
-        b[q] = rot ? w[p] * s[e] : 0.f;
+        const float wp = w[INTER ? 2 * e : e], wq = w[INTER ? 2 * e + 1 : 8 + e];
+        a[e >> 2][e & 3] = rot ? wp * c[e] : wp;
+        a[2 + (e >> 2)][e & 3] = rot ? wq * c[e] : wq;
+        a[4 + (e >> 2)][e & 3] = rot ? -wq * s[e] : 0.f;
+        a[6 + (e >> 2)][e & 3] = rot ? wp * s[e] : 0.f;
     }
 #pragma unroll
-    for (int f = 0; f < 4; ++f) {
-        k[f * stride] = make_float4(a[4 * f], a[4 * f + 1], a[4 * f + 2], a[4 * f + 3]);
-        k[(4 + f) * stride] = make_float4(b[4 * f], b[4 * f + 1], b[4 * f + 2], b[4 * f + 3]);
-    }
+    for (int f = 0; f < 8; ++f) k[f * stride] = make_float4(a[f][0], a[f][1], a[f][2], a[f][3]);
 }
 
-// A lane's values (x: octet a, y: octet b) normed by r, weighted and rotated. `full`: every lane of the row is
-// rotated (uniform). Otherwise a lane that is not takes no part of its neighbour, not even 0 times infinity.
-template <bool INTER>
-__device__ __forceinline__ void row_apply(float* x, float* y, float r, bool rot, bool full, const float4* k,
-                                          int stride) {
+// A lane's values normed by r, weighted and rotated. `full`: every lane of the row is rotated (uniform).
+// Otherwise a lane that is not takes no part of its partner, not even 0 times infinity.
+__device__ __forceinline__ void row_apply(RowPairs& v, float r, bool rot, bool full, const float4* k, int stride) {
+    const F2 r2 = f2(r, r);
     auto apply = [&](auto all) {
-        auto pair = [&](float& u, float& v, float au, float av, float bu, float bv) {
-            const float p = u * r, q = v * r;
-            float s = q * bu, t = p * bv;
-            if constexpr (!decltype(all)::value) {
-                s = rot ? s : 0.f;
-                t = rot ? t : 0.f;
-            }
-            u = fmaf(p, au, s);
-            v = fmaf(q, av, t);
-        };
 #pragma unroll
-        for (int f = 0; f < (INTER ? 4 : 2); ++f) {
-            if constexpr (INTER) {
-                const float4 a = k[f * stride], b = k[(4 + f) * stride];
-                float* v = (f < 2 ? x : y) + 4 * (f & 1);
-                pair(v[0], v[1], a.x, a.y, b.x, b.y);
-                pair(v[2], v[3], a.z, a.w, b.z, b.w);
-            } else {
-                const float4 au = k[f * stride], av = k[(2 + f) * stride], bu = k[(4 + f) * stride], bv = k[(6 + f) * stride];
-                pair(x[4 * f], y[4 * f], au.x, av.x, bu.x, bv.x);
-                pair(x[4 * f + 1], y[4 * f + 1], au.y, av.y, bu.y, bv.y);
-                pair(x[4 * f + 2], y[4 * f + 2], au.z, av.z, bu.z, bv.z);
-                pair(x[4 * f + 3], y[4 * f + 3], au.w, av.w, bu.w, bv.w);
+        for (int f = 0; f < 2; ++f) {
+            const float4 pp = k[f * stride], qq = k[(2 + f) * stride], pq = k[(4 + f) * stride], qp = k[(6 + f) * stride];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const F2 p = f2_mul(v.p[2 * f + i], r2), q = f2_mul(v.q[2 * f + i], r2);
+                F2 s = f2_mul(q, i ? f2(pq.z, pq.w) : f2(pq.x, pq.y)), t = f2_mul(p, i ? f2(qp.z, qp.w) : f2(qp.x, qp.y));
+                if constexpr (!decltype(all)::value) {
+                    s.v = rot ? s.v : 0ull;
+                    t.v = rot ? t.v : 0ull;
+                }
+                v.p[2 * f + i] = f2_fma(p, i ? f2(pp.z, pp.w) : f2(pp.x, pp.y), s);
+                v.q[2 * f + i] = f2_fma(q, i ? f2(qq.z, qq.w) : f2(qq.x, qq.y), t);
             }
         }
     };

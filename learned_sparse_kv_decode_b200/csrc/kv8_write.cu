@@ -43,19 +43,18 @@ __device__ __forceinline__ void prep_heads(const uint8_t* src, uint8_t* dst, int
         rb = octet_load<BF16>(src, ob);
     }
     for (int u = h0; u < h1; u += 4) {  // uniform in the warp: the norm's shuffles need every lane
-        float x[8], y[8];
-        octet_floats<BF16>(ra, x);
-        octet_floats<BF16>(rb, y);
+        RowPairs v = row_pairs<BF16, INTER>(ra, rb);
         src += 4 * kRow;
         if (h + 4 < h1) {
             ra = octet_load<BF16>(src, oa);
             rb = octet_load<BF16>(src, ob);
         }
-        const float r = norm ? row_rms(x, y, eps) : 1.f;
-        row_apply<INTER>(x, y, r, rot, full, k, 8);
+        row_apply(v, norm ? row_rms(v, eps) : 1.f, rot, full, k, 8);
         if (h < h1) {
-            octet_store<BF16>(dst, oa, x);
-            octet_store<BF16>(dst, ob, y);
+            OctetRaw<BF16> xa, xb;
+            row_octets_of<BF16, INTER>(v, &xa, &xb);
+            octet_store<BF16>(dst, oa, xa);
+            octet_store<BF16>(dst, ob, xb);
         }
         dst += 4 * kRow;
         h += 4;
@@ -262,14 +261,11 @@ __device__ __forceinline__ void append_heads(AppendRow w, const PrepParams& pp, 
         }
         const float was = !ALL && w.has_old ? *w.scale : 0.f;  // read before the barrier, written after it
         if constexpr (PREP != 0) {
-            float x[8], y[8];
-            octet_floats<BF16>(xa, x);
-            octet_floats<BF16>(xb, y);
-            const float rms = norm ? row_rms(x, y, eps) : 1.f;
+            RowPairs v = row_pairs<BF16, INTER>(xa, xb);
+            const float rms = norm ? row_rms(v, eps) : 1.f;
             if (ALL || w.fresh) {
-                row_apply<INTER>(x, y, rms, rot, full, coef, kAppendThreads);
-                xa = octet_pack<BF16>(x);  // what lsa_qk_norm_rope would have stored
-                xb = octet_pack<BF16>(y);
+                row_apply(v, rms, rot, full, coef, kAppendThreads);
+                row_octets_of<BF16, INTER>(v, &xa, &xb);  // what lsa_qk_norm_rope would have stored
             }
         }
         uint32_t top = warp_amax<BF16>(xa, xb, err);
