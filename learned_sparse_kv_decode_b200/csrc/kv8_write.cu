@@ -109,7 +109,7 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
 constexpr int kAppendThreads = 512;
 constexpr int kAppendRows = kAppendThreads / 8;
 constexpr int kAppendCoefBytes = 8 * kAppendThreads * 16;
-constexpr int kAppendCtas = 8;  // CTAs per SM that a long call is cut into
+constexpr int kAppendCtas = 16, kAppendPrepCtas = 8;  // CTAs per SM that a long call is cut into
 
 struct AppendParams {
     Kv8Geom g;
@@ -329,6 +329,10 @@ k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uin
         w.pos = (int32_t)pos;
         const int64_t row_in = (int64_t)b * ap.n_new + (pos - start);
         w.src = (is_v ? ap.v + row_in * ap.v_stride : ap.k + row_in * ap.k_stride) + (int64_t)h0 * kRow;
+        // A head's rows are short runs far apart: the slice's heads of a row, which follow one another, are
+        // brought to L2 in one request (99 -> 91 us for the largest prepared append).
+        if (w.n_h > 1 && w.fresh && (tid & 7) == 0)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w.src), "r"(w.n_h * kRow) : "memory");
         const int within = (int)(pos & ((1 << ap.g.c_log2) - 1));
         const int64_t ch0 = (tab.chunk_off[b] + (pos >> ap.g.c_log2)) * ap.g.Hkv + h0;
         w.dst = (is_v ? ap.V8 : ap.K8) + ((ch0 << ap.g.c_log2) + within) * kDh;
@@ -429,9 +433,11 @@ cudaError_t launch_kv8_append(const lsa_dims& d, const SeqTable& tab, const lsa_
     ap.n_new = n_new;
     // a run of n tokens touches at most (n + 62) / 64 + 1 aligned windows (one token: one)
     ap.windows = (int)(((int64_t)n_new + 62) / 64 + 1);
-    // Long slices while there are CTAs enough: the angles are computed once for a slice's heads, and a head's
-    // rows are loaded during the one before.
-    const int64_t cells = (int64_t)ap.windows * d.B * 2, want = (int64_t)num_sms * kAppendCtas;
+    // Long slices of heads while there are CTAs enough: a row's heads follow one another in memory, and K's
+    // angles are computed once for a slice. Measured on 4 x 8192 tokens, 16 heads, with 4, 8 and 16 CTAs per SM
+    // (K's and V's together): rows that are only quantised 86, 73 and 65 us, prepared rows 105, 91 and 96.
+    const int64_t cells = (int64_t)ap.windows * d.B * 2;
+    const int64_t want = (int64_t)num_sms * (prep != nullptr ? kAppendPrepCtas : kAppendCtas);
     int64_t slices = cells >= want ? 1 : (want + cells - 1) / cells;
     if (slices > g.Hkv) slices = g.Hkv;
     ap.per = (int)((g.Hkv + slices - 1) / slices);
