@@ -412,42 +412,57 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         // ---- O^T = O^T alpha + V^T P^T
         cp_async_wait<1>();
         __syncwarp();  // every lane's copies of V have landed
-        uint4 vv[8];
+        // PLO: 16 tokens at a time, each added to the output on its own, for the low halves' registers
+        constexpr int HALVES = PLO ? 2 : 1, NE = 2 / HALVES;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            vv[2 * i] = kv8_lds16(va0 + i * 8 * kDh);
-            vv[2 * i + 1] = kv8_lds16(va1 + i * 8 * kDh);
-        }
-        if (!whole) {  // rows behind the sequence may hold anything: a weight of 0 does not undo a NaN
+        for (int half = 0; half < HALVES; ++half) {
+            uint4 vv[4 * NE];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = (int)kv8_lds(mb + 256 + 4 * i);
-                if (2 * t >= n) vv[2 * i] = make_uint4(0, 0, 0, 0);
-                if (2 * t + 1 >= n) vv[2 * i + 1] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 2 * NE; ++i) {
+                vv[2 * i] = kv8_lds16(va0 + (2 * half + i) * 8 * kDh);
+                vv[2 * i + 1] = kv8_lds16(va1 + (2 * half + i) * 8 * kDh);
             }
-        }
-        __syncwarp();  // the V rows are read
-        copy(it + 1, p.V8, kKv8SlotV);
+            if (!whole) {  // rows behind the sequence may hold anything: a weight of 0 does not undo a NaN
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float c[4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {  // tokens 0..15, 16..31 of the tile
-                    const uint32_t y0 = __byte_perm((&vv[4 * e].x)[w], (&vv[4 * e + 1].x)[w], i ? 0x7362 : 0x5140);
-                    const uint32_t y1 = __byte_perm((&vv[4 * e + 2].x)[w], (&vv[4 * e + 3].x)[w], i ? 0x7362 : 0x5140);
-                    const uint32_t b0 = e4m3lo_f16x2(y0), b1 = e4m3hi_f16x2(y0);
-                    const uint32_t b2 = e4m3lo_f16x2(y1), b3 = e4m3hi_f16x2(y1);
-                    if (e == 0) mma_f16(c, b0, b1, b2, b3, ph[0], ph[1], zero);
-                    else mma_f16(c, b0, b1, b2, b3, ph[2], ph[3], c);
-                    if constexpr (PLO) mma_f16(c, b0, b1, b2, b3, pl[2 * e], pl[2 * e + 1], c);
+                for (int i = 0; i < 2 * NE; ++i) {
+                    const int n = (int)kv8_lds(mb + 256 + 4 * (2 * half + i));
+                    if (2 * t >= n) vv[2 * i] = make_uint4(0, 0, 0, 0);
+                    if (2 * t + 1 >= n) vv[2 * i + 1] = make_uint4(0, 0, 0, 0);
                 }
-                float(&oo)[4] = o[2 * w + i];
-                oo[0] = fmaf(oo[0], a0, c[0]);
-                oo[1] = fmaf(oo[1], a1, c[1]);
-                oo[2] = fmaf(oo[2], a0, c[2]);
-                oo[3] = fmaf(oo[3], a1, c[3]);
+            }
+            if (half == HALVES - 1) {
+                __syncwarp();  // the V rows are read
+                copy(it + 1, p.V8, kKv8SlotV);
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float c[4];
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) {  // 16 tokens
+                        const int k = 2 * (half + e);
+                        const uint32_t y0 = __byte_perm((&vv[4 * e].x)[w], (&vv[4 * e + 1].x)[w], i ? 0x7362 : 0x5140);
+                        const uint32_t y1 = __byte_perm((&vv[4 * e + 2].x)[w], (&vv[4 * e + 3].x)[w], i ? 0x7362 : 0x5140);
+                        const uint32_t b0 = e4m3lo_f16x2(y0), b1 = e4m3hi_f16x2(y0);
+                        const uint32_t b2 = e4m3lo_f16x2(y1), b3 = e4m3hi_f16x2(y1);
+                        if (e == 0) mma_f16(c, b0, b1, b2, b3, ph[k], ph[k + 1], zero);
+                        else mma_f16(c, b0, b1, b2, b3, ph[k], ph[k + 1], c);
+                        if constexpr (PLO) mma_f16(c, b0, b1, b2, b3, pl[k], pl[k + 1], c);
+                    }
+                    float(&oo)[4] = o[2 * w + i];
+                    if (half == 0) {
+                        oo[0] = fmaf(oo[0], a0, c[0]);
+                        oo[1] = fmaf(oo[1], a1, c[1]);
+                        oo[2] = fmaf(oo[2], a0, c[2]);
+                        oo[3] = fmaf(oo[3], a1, c[3]);
+                    } else {
+                        oo[0] += c[0];
+                        oo[1] += c[1];
+                        oo[2] += c[2];
+                        oo[3] += c[3];
+                    }
+                }
             }
         }
     }
