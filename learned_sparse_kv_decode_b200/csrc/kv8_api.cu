@@ -151,9 +151,9 @@ lsa_status lsa_qk_norm_rope(const lsa_dims* dims, int32_t n_kv_heads, const lsa_
     if (s != LSA_OK) return s;
     if (n_tok < 0 || n_tok > (1ll << 31)) return LSA_ERR_INVALID_ARG;
     if (!is_pow2(n_kv_heads) || n_kv_heads > dims->H) return LSA_ERR_UNSUPPORTED;
+    if (n_tok == 0) return LSA_OK;
     if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr)) return LSA_ERR_INVALID_ARG;
     if (q == nullptr && k == nullptr) return LSA_ERR_INVALID_ARG;
-    if (n_tok == 0) return LSA_OK;
     if (positions == nullptr || !aligned4(positions)) return LSA_ERR_INVALID_ARG;
     if (q != nullptr && (!aligned16(q) || !aligned16(q_out) || !stride_ok(dims, dims->H, q_stride) ||
                          !stride_ok(dims, dims->H, q_out_stride) || (q == q_out && q_stride != q_out_stride)))

@@ -252,56 +252,47 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     copy(0, p.K8, 0);
     copy(0, p.V8, kKv8SlotV);
 
-    // ---- q: row g % rows, scaled to stay below 2^15, as f16 hi + lo; each of four warps does two steps'
-    // share of the 128 values (8 per lane)
-    float qmul;
-    {
-        const int64_t at = (int64_t)(qrow0 + (g & (p.rows - 1))) * kDh + t * 32;
-        auto load = [&](int i, float* x) {  // values 8 i .. 8 i + 7 of the lane's 32
-            octet_floats<BF16>(octet_load<BF16>(p.q + at * (BF16 ? 2 : 4), i), x);
-        };
-        float top = 0.f;
-        bool nan = false;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            float x[8];
-            load(s, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                top = fmaxf(top, fabsf(x[e]));
-                nan |= x[e] != x[e];
-            }
+    // ---- q: rows scaled to stay below 2^15, as f16 hi + lo. A warp splits a row at a time: a lane's four values
+    // are one step's share of lane (row, lane / 8) in the 16-row operand, hi in rows 0..7 and lo in rows 8..15.
+    // With fewer than 8 heads the rows recur.
+    __shared__ float s_qmul[kKv8MaxRows];
+    for (int c = warp; c < kKv8MaxRows; c += WARPS) {
+        const int r = c & (p.rows - 1);
+        float x[4];
+        if constexpr (BF16) {
+            const uint2 v = reinterpret_cast<const uint2*>(p.q)[(int64_t)(qrow0 + r) * 32 + lane];
+            x[0] = bf16lo(v.x); x[1] = bf16hi(v.x); x[2] = bf16lo(v.y); x[3] = bf16hi(v.y);
+        } else {
+            const float4 v = reinterpret_cast<const float4*>(p.q)[(int64_t)(qrow0 + r) * 32 + lane];
+            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the largest magnitude's bits; what is not finite is above the rest
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+        top = __reduce_max_sync(0xffffffffu, top);
         // top < 2^(ex + 1): times 2^(14 - ex) it stays below 2^15. The factor is kept within fp32.
-        int ex = (int)(__float_as_uint(top) >> 23) - 127;
+        int ex = (int)(top >> 23) - 127;
         ex = ex < -110 ? -110 : ex;
         const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-        qmul = p.qscale * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
-        // a row with an infinity or a NaN has no finite scores
-        const uint32_t bad = __ballot_sync(0xffffffffu, nan || !(top < INFINITY));
-        if (bad >> (lane & 28) & 15) qmul = __uint_as_float(0x7fc00000u);
-        if (warp < 4) {
-            float y[8];
-            load(warp, y);
+        uint32_t a[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {  // the 16-row operand of step 2 warp + i: hi in rows 0..7, lo in rows 8..15
-                uint32_t a[4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float x0 = y[4 * i + 2 * j] * up, x1 = y[4 * i + 2 * j + 1] * up;
-                    a[2 * j] = f16x2_rn(x0, x1);
-                    const float2 f = f16x2_floats(a[2 * j]);
-                    a[2 * j + 1] = f16x2_rn(x0 - f.x, x1 - f.y);
-                }
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + (2 * warp + i) * 512), "r"(a[0]),
-                             "r"(a[1]), "r"(a[2]), "r"(a[3])
-                             : "memory");
-            }
+        for (int j = 0; j < 2; ++j) {
+            const float x0 = x[2 * j] * up, x1 = x[2 * j + 1] * up;
+            a[2 * j] = f16x2_rn(x0, x1);
+            const float2 f = f16x2_floats(a[2 * j]);
+            a[2 * j + 1] = f16x2_rn(x0 - f.x, x1 - f.y);
         }
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs - 16 * lane + (lane & 7) * 512 + (4 * c + (lane >> 3)) * 16),
+                     "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3])
+                     : "memory");
+        // a row with an infinity or a NaN has no finite scores
+        if (lane == 0)
+            s_qmul[c] = top < 0x7F800000u ? p.qscale * __uint_as_float((uint32_t)(ex - 14 + 127) << 23)
+                                          : __uint_as_float(0x7FC00000u);
     }
     __syncthreads();
+    const float qmul = s_qmul[g];
 
     float o[8][4], m = -INFINITY, l = 0.f, vref = 0.f;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
@@ -496,25 +487,58 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         }
     }
     __syncthreads();
-    for (int i = tid; i < p.rows * kDh; i += WARPS * 32) {
-        const int r = i >> 7, d = i & (kDh - 1);
-        float M = -INFINITY, A = 0.f, L = 0.f;
+    // Each thread sums four columns of a row over the warps. A row's maximum, sum and factors: with one or two
+    // rows every thread works them out for itself, with more a warp does it for all.
+    const bool shared_factors = p.rows > 2;
+    if (shared_factors) {
+        for (int r = warp; r < p.rows; r += WARPS) {
+            const float mw = lane < WARPS ? s_ml[lane & (WARPS - 1)][r][0] : -INFINITY;
+            float M = mw;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][r][0]);
+            for (int k = 1; k < WARPS; k <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+            const float f = mw == -INFINITY ? 0.f : kv8_ex2(mw - M);
+            float L = lane < WARPS ? f * s_ml[lane & (WARPS - 1)][r][1] : 0.f;
+#pragma unroll
+            for (int k = 1; k < WARPS; k <<= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+            __syncwarp();
+            if (lane < WARPS) s_ml[lane][r][0] = f;
+            if (lane == 0) {
+                s_ml[0][r][1] = L;
+                s_qmul[r] = M;
+            }
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < p.rows * (kDh / 4); i += WARPS * 32) {
+        const int r = i >> 5, d = (i & 31) * 4;
+        float M = -INFINITY, L = 0.f;
+        if (shared_factors) {
+            M = s_qmul[r];
+            L = s_ml[0][r][1];
+        } else {
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][r][0]);
+        }
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            const float mw = s_ml[w][r][0];
-            const float f = mw == -INFINITY ? 0.f : kv8_ex2(mw - M);
-            A = fmaf(f, s_o[w][r][d], A);
-            L = fmaf(f, s_ml[w][r][1], L);
+            float f = s_ml[w][r][0];
+            if (!shared_factors) {
+                f = f == -INFINITY ? 0.f : kv8_ex2(f - M);
+                L = fmaf(f, s_ml[w][r][1], L);
+            }
+            const float4 v = *reinterpret_cast<const float4*>(&s_o[w][r][d]);
+            A.x = fmaf(f, v.x, A.x); A.y = fmaf(f, v.y, A.y);
+            A.z = fmaf(f, v.z, A.z); A.w = fmaf(f, v.w, A.w);
         }
         if (parts == 1) {
-            p.out[(int64_t)(qrow0 + r) * kDh + d] = L == 0.f ? 0.f : A / L;
+            *reinterpret_cast<float4*>(p.out + (int64_t)(qrow0 + r) * kDh + d) =
+                L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(A.x / L, A.y / L, A.z / L, A.w / L);
             if (d == 0 && p.lse != nullptr)
                 p.lse[qrow0 + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
         } else {
             const int64_t at = (int64_t)blockIdx.x * kKv8MaxRows + r;
-            p.part_o[at * kDh + d] = A;
+            *reinterpret_cast<float4*>(p.part_o + at * kDh + d) = A;
             if (d == 0) {
                 p.part_ml[at * 2] = M;
                 p.part_ml[at * 2 + 1] = L;
@@ -666,20 +690,19 @@ static int kv8_part_tiles(const Kv8Tab& t, int c_log2, int64_t runs_b, int64_t s
 }
 
 // Microseconds that the runs take in parts of `per` tiles, `slots` CTAs at a time: the larger of what the
-// fullest SM computes (0.2 a tile while its 16 warps have one each, 0.137 from then on) and what memory reads
-// (8 KB a tile at 7 TB/s), 3.3 for a round of CTAs to start and to join its warps, 2 where runs are left to be
-// joined and 0.8 for the host to launch that. Measured: 8 runs of 8 tiles 4.9 us as 8 CTAs of 16 warps; of 16 tiles 6.6 so, of 32 tiles 6.2 as 64
+// fullest SM computes (0.2 a tile while its 16 warps have one each, 0.137 from then on; 3.3 for a round of
+// CTAs to start and to join its warps) and what memory reads (8 KB a tile at 7 TB/s), and, where runs are left
+// to be joined, 2 for that and 0.8 for the host to launch it. Measured: 8 runs of 8 tiles 4.9 us as 8 CTAs of 16 warps; of 16 tiles 6.6 so, of 32 tiles 6.2 as 64
 // CTAs of 4 warps; 128 runs of 16 tiles 7.3 as 128 wide CTAs, 8.3 as 256 of 4 warps.
 static double kv8_estimate(const Kv8Tab& t, int c_log2, int64_t runs_b, int per, int64_t all, int num_sms,
                            int64_t slots) {
     int64_t ctas = 0;
     for (int b = 0; b < t.B; ++b) ctas += runs_b * ((kv8_tiles(t, b, c_log2) + per - 1) / per);
-    const int64_t share = (all + num_sms - 1) / num_sms;
-    const int64_t load = ctas > slots ? (share > per ? share : per) : per * ((ctas + num_sms - 1) / num_sms);
-    const double compute = load < 16 ? 0.2 * (double)load : 1. + 0.137 * (double)load;
-    const double memory = 0.00117 * (double)all;
-    return (compute > memory ? compute : memory) + 3.3 * (double)((ctas + slots - 1) / slots) +
-           (ctas > runs_b * t.B ? 2.8 : 0.);
+    const int64_t rounds = (ctas + slots - 1) / slots, per_sm = (ctas + num_sms - 1) / num_sms, full = slots / num_sms;
+    const double load = (double)per * (double)(per_sm < full ? per_sm : full);
+    const double compute = load < 16. ? 0.2 * load : 1. + 0.137 * load;
+    const double memory = 3.3 + 0.00117 * (double)all, busy = (double)rounds * (3.3 + compute);
+    return (busy > memory ? busy : memory) + (ctas > runs_b * t.B ? 2.8 : 0.);
 }
 
 template <bool BF16, bool PLO>

@@ -69,17 +69,26 @@ def _shape(dims):
     return s
 
 
-def _ptr(t, name, dtype, numel, device):
-    """Data pointer of a contiguous tensor of `numel` elements on `device`."""
+def _where(index):
+    return "the CPU" if index < 0 else f"cuda:{index}"
+
+
+def _refuse(t, name, dtype, device):
+    """Raise for a tensor of another type or place than the call needs."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: expected a tensor on {_where(device)}, got one on {_where(t.get_device())}")
+
+
+def _ptr(t, name, dtype, numel, device):
+    """Data pointer of a contiguous tensor of `numel` elements on CUDA device `device`."""
+    if t.dtype is dtype and t.get_device() == device and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    if t.numel() != numel:
-        raise ValueError(f"{name}: expected {numel} elements, got {t.numel()}")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected {numel} elements, got {t.numel()}")
 
 
 def _opt(t, name, dtype, numel, device):
@@ -88,28 +97,27 @@ def _opt(t, name, dtype, numel, device):
 
 def _rows(t, name, dtype, rows, heads, device):
     """(pointer, elements from one row to the next) of rows [...][heads][Dh] whose heads lie side by side."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.dtype is not dtype or t.get_device() != device:
+        _refuse(t, name, dtype, device)
     shape, row = t.shape, heads * LSA_HEAD_DIM
-    if len(shape) < 3 or shape[-1] != LSA_HEAD_DIM or shape[-2] != heads or t.numel() != rows * row:
+    n = len(shape)
+    if n < 3 or t.numel() != rows * row or shape[n - 1] != LSA_HEAD_DIM or shape[n - 2] != heads:
         raise ValueError(f"{name}: expected {rows} rows of [{heads}][{LSA_HEAD_DIM}], got {tuple(shape)}")
     if t.is_contiguous():
         return t.data_ptr(), row
     stride = t.stride()
-    if stride[-1] != 1 or (heads > 1 and stride[-2] != LSA_HEAD_DIM):
+    if stride[n - 1] != 1 or (heads > 1 and stride[n - 2] != LSA_HEAD_DIM):
         raise ValueError(f"{name}: the values of a row must lie side by side")
     step, span = row, 1
-    for i in range(len(shape) - 3, -1, -1):
-        n, s = shape[i], stride[i]
-        if n == 1:
+    for i in range(n - 3, -1, -1):
+        size = shape[i]
+        if size == 1:
             continue
         if span == 1:
-            step = s
-        elif s != step * span:
+            step = stride[i]
+        elif stride[i] != step * span:
             raise ValueError(f"{name}: the rows must be evenly spaced")
-        span *= n
+        span *= size
     return t.data_ptr(), step
 
 
@@ -120,22 +128,23 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _stream(stream, device):
     if stream is None:
-        return _raw_stream(device.index)
+        return _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _device(t):
-    d = t.device
-    if d.type != "cuda":
+    """Index of the tensor's CUDA device, which has to be the current one."""
+    d = t.get_device()
+    if d < 0:
         raise ValueError("expected CUDA tensors")
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {d}, but the current device is cuda:{torch.cuda.current_device()}")
+    if d != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{d}, but the current device is cuda:{torch.cuda.current_device()}")
     return d
 
 
 def _ws(ws, device):
-    if ws.device != device:
-        raise ValueError(f"ws: expected a tensor on {device}, got {ws.device}")
+    if ws.get_device() != device:
+        raise ValueError(f"ws: expected a tensor on {_where(device)}, got one on {_where(ws.get_device())}")
     if not ws.is_contiguous():
         raise ValueError("ws: expected a contiguous tensor")
     return ws.data_ptr(), ws.numel() * ws.element_size()
@@ -153,8 +162,8 @@ class Kv8Cache:
         if self.n_kv_heads < 1 or self.scale_block < 1:
             raise abi.LsaError(abi.LSA_ERR_UNSUPPORTED, "Kv8Cache")
         self.chunks, self.C = s.chunks, s.C
-        self.device = K8.device
-        if self.device.type != "cuda":
+        self.device = K8.get_device()
+        if self.device < 0:
             raise ValueError("expected CUDA tensors")
         n = s.chunks * self.n_kv_heads * s.C
         ptrs = []
@@ -191,8 +200,8 @@ class QkPrep:
 
     def __init__(self, rot_dim, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False):
         ref = next((t for t in (inv_freq, q_weight, k_weight) if t is not None), None)
-        self.device = None if ref is None else ref.device
-        if ref is not None and self.device.type != "cuda":
+        self.device = None if ref is None else ref.get_device()
+        if ref is not None and self.device < 0:
             raise ValueError("expected CUDA tensors")
         f32 = torch.float32
         self.tensors = (inv_freq, q_weight, k_weight)
@@ -204,7 +213,7 @@ class QkPrep:
 
     def check(self, device):
         if self.device is not None and self.device != device:
-            raise ValueError(f"prep: expected tensors on {device}, got {self.device}")
+            raise ValueError(f"prep: expected tensors on {_where(device)}, got some on {_where(self.device)}")
         return self.ptr
 
 

@@ -98,6 +98,30 @@ def test_norm_rope(lsa, T, H, Hkv, dtype, rot, inter, norm, far):
     assert torch.equal(both[:, H + Hkv:], qkv[:, H + Hkv:])
 
 
+def test_norm_rope_of_no_tokens(lsa):
+    d = lsa.Dims(1, 1, 128, 4, 64, N=1, k=1, kv_dtype="f32")
+    x = torch.empty(0, 4, DH, device="cuda")
+    lsa.lsa_qk_norm_rope(d, lsa.QkPrep(0), i32([]), x, x[:, :2], x, x[:, :2])
+
+
+def test_norm_rope_infinities_stay_in_their_pairs(lsa):
+    """Without a norm, an infinity reaches its own pair and no other value; with one its row, and no other row."""
+    d = lsa.Dims(1, 1, 128, 2, 64, N=1, k=1, kv_dtype="f32")
+    inv = torch.linspace(1.0, 0.001, 32, device="cuda")
+    for inter in (False, True):
+        x = torch.randn(3, 2, DH, device="cuda")
+        x[1, 0, 5] = float("inf")    # rotated
+        x[1, 1, 70] = float("-inf")  # not rotated: rot_dim 64
+        o = torch.empty_like(x)
+        lsa.lsa_qk_norm_rope(d, lsa.QkPrep(64, inv, None, None, 1e-6, inter), i32([3, 4, 5]), x, None, o, None)
+        bad = ~torch.isfinite(o)
+        assert bad[1, 0].nonzero().view(-1).tolist() == ([4, 5] if inter else [5, 37])
+        assert bad[1, 1].nonzero().view(-1).tolist() == [70] and not bool(bad[[0, 2]].any())
+        lsa.lsa_qk_norm_rope(d, lsa.QkPrep(64, inv, torch.ones(DH, device="cuda"), None, 1e-6, inter), i32([3, 4, 5]),
+                             x, None, o, None)
+        assert bool(torch.isfinite(o[[0, 2]]).all())
+
+
 def test_norm_rope_zero_rows_and_negative_positions(lsa):
     d = lsa.Dims(1, 1, 128, 2, 64, N=1, k=1, kv_dtype="f32")
     x = torch.zeros(2, 2, DH, device="cuda")
@@ -366,6 +390,7 @@ ATTN = [
     ([40, 60], [33, 60], 64, 16, 1, 32, "f32", [2551, 3840], "free"),  # 16 query heads on one K/V head
     ([12], [12], 64, 128, 4, 64, "bf16", [700], "append"),             # 32 query heads on one
     ([300], [211], 32, 8, 8, 32, "bf16", None, "free"),
+    ([20, 9], [20, 3], 32, 128, 1, 8, "f32", [633, 280], "wide"),      # 128 query heads on one
     ([5, 4], [5, 2], 1024, 8, 4, 64, "f32", [5000, 1025], "wide"),
     ([1500], [1500], 64, 1, 1, 64, "bf16", None, "append"),            # one run across every CTA
     ([900, 700], [800, 5], 64, 8, 1, 64, "f32", [57600, 44799], "free"),

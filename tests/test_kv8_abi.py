@@ -108,8 +108,9 @@ def test_norm_rope_arguments_refused(kw, expect):
 
 
 def test_norm_rope_of_no_tokens_is_nothing():
-    assert abi.lib.lsa_qk_norm_rope(dims().ptr, 4, ref(prep()), 0, None, P, 2048, P, 512, P, 2048, P, 512,
-                                    None) == lsa.LSA_OK
+    for q in (P, None):  # an empty tensor's pointer may be null
+        assert abi.lib.lsa_qk_norm_rope(dims().ptr, 4, ref(prep()), 0, None, q, 2048, q, 512, q, 2048, q, 512,
+                                        None) == lsa.LSA_OK
 
 
 @pytest.mark.parametrize("kw,expect", [
@@ -175,7 +176,7 @@ def test_binding_refuses_host_tensors():
 
 
 def test_binding_checks_types_shapes_and_devices():
-    cpu = torch.device("cpu")
+    cpu = -1  # a CPU tensor's device index
     x = torch.zeros(6, 4)
     with pytest.raises(TypeError, match="float32"):
         kv8._ptr(x.half(), "x", torch.float32, 24, cpu)
@@ -184,19 +185,23 @@ def test_binding_checks_types_shapes_and_devices():
     with pytest.raises(ValueError, match="contiguous"):
         kv8._ptr(x.t(), "x", torch.float32, 24, cpu)
     with pytest.raises(ValueError, match="cuda:1"):
-        kv8._ptr(x, "x", torch.float32, 24, torch.device("cuda:1"))
+        kv8._ptr(x, "x", torch.float32, 24, 1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        kv8._rows(x.view(1, 6, 4), "x", torch.float32, 1, 6, 1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        kv8._ws(x, 1)
     assert kv8._opt(None, "x", torch.float32, 24, cpu) is None
 
 
 def test_binding_refuses_another_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    there = types.SimpleNamespace(device=torch.device("cuda:1"))
+    there = types.SimpleNamespace(get_device=lambda: 1)
     with pytest.raises(ValueError, match="current device"):
         kv8._device(there)
 
 
 def test_binding_row_strides():
-    f32, cpu = torch.float32, torch.device("cpu")
+    f32, cpu = torch.float32, -1
     qkv = torch.zeros(3, 5, 12, 128)  # [B][n][heads]
     assert kv8._rows(qkv[:, :, 4:8], "k", f32, 15, 4, cpu)[1] == 12 * 128
     assert kv8._rows(qkv[:1, :, 4:8], "k", f32, 5, 4, cpu)[1] == 12 * 128
