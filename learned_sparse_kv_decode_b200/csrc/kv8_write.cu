@@ -12,11 +12,14 @@
 namespace lsa {
 
 // ---------------------------------------------------------------- norm and rotation
-// One warp per (token, slice of heads). The token's 64 angles are computed once per warp, two to a lane
-// (a tenth of a row's work each), and handed round by shuffles; weight and
-// rotation become one pair of coefficients a value, which serve all the slice's heads from shared memory
-// (in registers they would halve the warps in flight). The warp walks its slice four heads at a time, eight
-// lanes to a head: its loads and stores are 1 KB runs (bf16) of the token's row, one run ahead in flight.
+// A token's angles cost as much as a few of its rows, and weight and rotation become coefficients that serve
+// all its heads from shared memory (in registers they would halve the warps in flight). Two forms:
+//   a warp per (token, slice of heads): its lanes share the angles, two each, and it walks four heads at a
+//   time, in 1 KB runs (bf16) of the token's row;
+//   (MANY) with four heads or fewer and tokens enough, a warp per four tokens, eight lanes to a token, each with
+//   its own eight angles: a quarter of the coefficients' work.
+// In both the next rows are loaded while the ones before are worked on. 16384 tokens of 32 + 8 heads take 59 us
+// in the first form and 78 to 84 in the second (four rows far apart at a time), 27011 of 2 + 1 heads 25 and 14.
 constexpr int kPrepThreads = 128;
 
 struct PrepRows {
@@ -25,16 +28,15 @@ struct PrepRows {
     int64_t q_stride, k_stride, qo_stride, ko_stride;  // bytes from one token to the next
     int32_t H, Hkv;        // 0 where q or k is absent
     int64_t n_tok;
-    int32_t slices;        // warps per token
-    int32_t q_per, k_per;  // four-head units per slice
+    int32_t slices;        // warps per token, or per four
+    int32_t q_per, k_per;  // heads per slice
 };
 
-// Heads h0 + grp, + 4, ... below h1 of one token.
-template <bool BF16, bool INTER>
-__device__ __forceinline__ void prep_heads(const uint8_t* src, uint8_t* dst, int h0, int h1, int grp, int oa, int ob,
+// Heads h, h + step, ... below h1 of a token, n steps (uniform in the warp: the norm's shuffles need every lane).
+template <bool BF16, bool INTER, bool MANY>
+__device__ __forceinline__ void prep_heads(const uint8_t* src, uint8_t* dst, int h, int h1, int n, int oa, int ob,
                                            bool norm, float eps, bool rot, bool full, const float4* k) {
-    constexpr int kRow = kDh * (BF16 ? 2 : 4);
-    int h = h0 + grp;
+    constexpr int kRow = kDh * (BF16 ? 2 : 4), step = MANY ? 1 : 4;
     src += (int64_t)h * kRow;
     dst += (int64_t)h * kRow;
     OctetRaw<BF16> ra{}, rb{};
@@ -42,62 +44,70 @@ __device__ __forceinline__ void prep_heads(const uint8_t* src, uint8_t* dst, int
         ra = octet_load<BF16>(src, oa);
         rb = octet_load<BF16>(src, ob);
     }
-    for (int u = h0; u < h1; u += 4) {  // uniform in the warp: the norm's shuffles need every lane
+    for (int u = 0; u < n; ++u) {
         RowPairs v = row_pairs<BF16, INTER>(ra, rb);
-        src += 4 * kRow;
-        if (h + 4 < h1) {
+        src += step * kRow;
+        if (h + step < h1) {
             ra = octet_load<BF16>(src, oa);
             rb = octet_load<BF16>(src, ob);
         }
-        row_apply(v, norm ? row_rms(v, eps) : 1.f, rot, full, k, 8);
+        row_apply(v, norm ? row_rms(v, eps) : 1.f, rot, full, k, MANY ? 32 : 8);
         if (h < h1) {
             OctetRaw<BF16> xa, xb;
             row_octets_of<BF16, INTER>(v, &xa, &xb);
             octet_store<BF16>(dst, oa, xa);
             octet_store<BF16>(dst, ob, xb);
         }
-        dst += 4 * kRow;
-        h += 4;
+        dst += step * kRow;
+        h += step;
     }
 }
 
-template <bool BF16, bool INTER>
+template <bool BF16, bool INTER, bool MANY>
 __global__ void __launch_bounds__(kPrepThreads, BF16 ? 8 : 6)
 k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict__ positions) {
-    __shared__ float4 s_coef[kPrepThreads / 32][8][8];  // [warp][a, b][lane of the row]
+    constexpr int kLanes = MANY ? 32 : 8;
+    __shared__ float4 s_coef[kPrepThreads / 32][8][kLanes];  // [warp][which][lane of the row (MANY: and token)]
     pdl_trigger();
     const int lane = threadIdx.x & 31, sub = lane & 7, grp = lane >> 3;
     const int64_t w = (int64_t)blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
-    const int64_t tok = r.slices == 1 ? w : w / r.slices;
-    if (tok < r.n_tok) {
-        const int slice = (int)(w - tok * r.slices);
-        float c2[2] = {1.f, 1.f}, s2[2] = {0.f, 0.f};
-        if (pp.ho > 0) {
+    const int64_t cell = r.slices == 1 ? w : w / r.slices;
+    const int slice = (int)(w - cell * r.slices);
+    const int64_t tok = MANY ? 4 * cell + grp : cell;
+    if (cell * (MANY ? 4 : 1) < r.n_tok) {
+        const bool on = tok < r.n_tok;
+        const int q0 = slice * r.q_per, q1 = min(r.H, q0 + r.q_per), k0 = slice * r.k_per, k1 = min(r.Hkv, k0 + r.k_per);
+        const uint8_t *q = r.q + tok * r.q_stride, *kk = r.k + tok * r.k_stride;
+        const bool rot = sub < pp.ho, full = pp.ho == 8;
+        // MANY: the lane's eight angles; else two of the token's, handed round when coefficients are made
+        float c2[MANY ? 8 : 2], s2[MANY ? 8 : 2];
+        if (MANY ? on && rot : pp.ho > 0) {
             const int32_t pos = positions[tok];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (2 * lane + j < pp.ho * 8) angle_cs<BF16>(pos, pp.inv_freq[2 * lane + j], &c2[j], &s2[j]);
+            for (int j = 0; j < (MANY ? 8 : 2); ++j) {
+                const int a = MANY ? 8 * sub + j : 2 * lane + j;
+                if (MANY || a < pp.ho * 8) angle_cs<BF16>(pos, pp.inv_freq[a], &c2[j], &s2[j]);
+            }
         }
         int oa, ob;
         row_octets(sub, pp.ho, INTER, &oa, &ob);
-        const bool rot = sub < pp.ho, full = pp.ho == 8;
-        float4* k = &s_coef[threadIdx.x >> 5][0][sub];
-        auto heads = [&](const uint8_t* src, uint8_t* dst, int n, int per, const float* weight) {
-            const int h0 = slice * per * 4, h1 = min(n, h0 + per * 4);
+        float4* k = &s_coef[threadIdx.x >> 5][0][MANY ? lane : sub];
+        auto heads = [&](const uint8_t* src, uint8_t* dst, int h0, int h1, const float* weight) {
             if (h0 >= h1) return;
             float c[8], s[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                c[e] = __shfl_sync(0xffffffffu, c2[e & 1], sub * 4 + (e >> 1));
-                s[e] = __shfl_sync(0xffffffffu, s2[e & 1], sub * 4 + (e >> 1));
+                c[e] = MANY ? c2[MANY ? e : 0] : __shfl_sync(0xffffffffu, c2[e & 1], sub * 4 + (e >> 1));
+                s[e] = MANY ? s2[MANY ? e : 0] : __shfl_sync(0xffffffffu, s2[e & 1], sub * 4 + (e >> 1));
             }
             __syncwarp();  // the queries' coefficients are done with
-            if (grp == 0) row_coefs<INTER>(k, 8, weight, oa, ob, rot, c, s);
+            if (MANY || grp == 0) row_coefs<INTER>(k, kLanes, weight, oa, ob, rot, c, s);
             __syncwarp();
-            prep_heads<BF16, INTER>(src, dst, h0, h1, grp, oa, ob, weight != nullptr, pp.eps, rot, full, k);
+            prep_heads<BF16, INTER, MANY>(src, dst, MANY ? h0 : h0 + grp, on ? h1 : h0, MANY ? h1 - h0 : (h1 - h0 + 3) >> 2,
+                                          oa, ob, weight != nullptr, pp.eps, rot, full, k);
         };
-        heads(r.q + tok * r.q_stride, r.qo + tok * r.qo_stride, r.H, r.q_per, pp.q_weight);
-        heads(r.k + tok * r.k_stride, r.ko + tok * r.ko_stride, r.Hkv, r.k_per, pp.k_weight);
+        heads(q, r.qo + tok * r.qo_stride, q0, q1, pp.q_weight);
+        heads(kk, r.ko + tok * r.ko_stride, k0, k1, pp.k_weight);
     }
     pdl_wait();  // launched early, nothing above depends on the kernel before; the one after does
 }
@@ -384,15 +394,17 @@ cudaError_t launch_qk_norm_rope(const lsa_dims& d, int n_kv_heads, const lsa_qk_
     r.H = q != nullptr ? d.H : 0;
     r.Hkv = k != nullptr ? n_kv_heads : 0;
     r.n_tok = n_tok;
-    // a warp per token where there are tokens enough to fill the SMs, else the heads are split
-    const int qu = (r.H + 3) / 4, ku = (r.Hkv + 3) / 4;
-    const int64_t want = (int64_t)num_sms * 24;
-    int64_t slices = n_tok >= want ? 1 : (want + n_tok - 1) / n_tok;
-    if (slices > (qu > ku ? qu : ku)) slices = qu > ku ? qu : ku;
+    // A warp to a token (or, with few heads, to four) where there are tokens enough to fill the SMs, else the
+    // heads of a token are spread, four to a warp at the least.
+    const bool many = r.H <= 4 && r.Hkv <= 4 && n_tok >= (int64_t)num_sms * 4 * 24;
+    const int64_t cells = many ? (n_tok + 3) / 4 : n_tok, want = (int64_t)num_sms * 24;
+    const int unit = many ? 1 : 4, qu = (r.H + unit - 1) / unit, ku = (r.Hkv + unit - 1) / unit, most = qu > ku ? qu : ku;
+    int64_t slices = cells >= want ? 1 : (want + cells - 1) / cells;
+    if (slices > most) slices = most;
     r.slices = (int)slices;
-    r.q_per = (int)((qu + slices - 1) / slices);
-    r.k_per = (int)((ku + slices - 1) / slices);
-    const int64_t warps = n_tok * r.slices;
+    r.q_per = (int)((qu + slices - 1) / slices) * unit;
+    r.k_per = (int)((ku + slices - 1) / slices) * unit;
+    const int64_t warps = cells * r.slices;
     const int64_t ctas = (warps + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
     if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
@@ -405,11 +417,16 @@ cudaError_t launch_qk_norm_rope(const lsa_dims& d, int n_kv_heads, const lsa_qk_
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
     cfg.blockDim = dim3(kPrepThreads, 1, 1);
     const PrepParams pp = prep_params(&prep);
+    auto launch = [&](auto bf, auto inter, auto form) {
+        return cudaLaunchKernelEx(&cfg, k_qk_norm_rope<decltype(bf)::value, decltype(inter)::value, decltype(form)::value>, r,
+                                  pp, positions);
+    };
+    auto by_form = [&](auto bf, auto inter) {
+        return many ? launch(bf, inter, Const<true>{}) : launch(bf, inter, Const<false>{});
+    };
     if (d.kv_dtype == LSA_BF16)
-        return pp.interleaved ? cudaLaunchKernelEx(&cfg, k_qk_norm_rope<true, true>, r, pp, positions)
-                              : cudaLaunchKernelEx(&cfg, k_qk_norm_rope<true, false>, r, pp, positions);
-    return pp.interleaved ? cudaLaunchKernelEx(&cfg, k_qk_norm_rope<false, true>, r, pp, positions)
-                          : cudaLaunchKernelEx(&cfg, k_qk_norm_rope<false, false>, r, pp, positions);
+        return pp.interleaved ? by_form(Const<true>{}, Const<true>{}) : by_form(Const<true>{}, Const<false>{});
+    return pp.interleaved ? by_form(Const<false>{}, Const<true>{}) : by_form(Const<false>{}, Const<false>{});
 }
 
 // CTAs of an append, or 0 where they pass a grid's limit.

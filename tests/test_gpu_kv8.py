@@ -47,6 +47,9 @@ PREP = [
     (64, 128, 16, "bf16", 16, True, True, 100),
     (2, 8, 4, "bf16", 0, False, True, 100),
     (5000, 8, 2, "bf16", 128, False, True, 1 << 20),
+    (14211, 4, 1, "bf16", 64, True, True, 1 << 20),   # four tokens to a warp, the last warp with three
+    (14209, 1, 1, "f32", 128, False, True, 1 << 20),
+    (14210, 2, 2, "f32", 32, True, False, 1 << 20),
 ]
 
 
