@@ -192,21 +192,29 @@ __device__ __forceinline__ void load8(const float* p, float* w) {
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
-// Cosine and sine of position * f: the product and its reduction to a turn in 64 bits (positions of a
-// long context make angles of 2^20 rad and more, where 32 bits are off by tenths), the fraction in 32.
-// FAST, for rows that are rounded to bf16 (2^-9): the hardware's sine and cosine, within 2^-21 on [-pi, pi];
-// otherwise within 2 ulp, at four times the instructions.
-template <bool FAST>
+// Cosine and sine of position * f. The product and its reduction to within an eighth of a turn are in 64 bits
+// (positions of a long context make angles of 2^20 rad and more, where 32 bits are off by tenths); from there
+// the Taylor series about 0 suffice in 32: on [-pi/4, pi/4] the first omitted terms, x^11 / 11! and x^12 / 12!,
+// are below 2e-9, and the result is within 2^-23.
 __device__ __forceinline__ void angle_cs(int32_t position, float f, float* c, float* s) {
-    double t = (double)position * (double)f * 0.15915494309189534;  // 1 / (2 pi)
-    t -= rint(t);
-    if constexpr (FAST) {
-        const float a = (float)t * 6.2831853071795865f;
-        *s = __sinf(a);
-        *c = __cosf(a);
-    } else {
-        sincospif((float)(2.0 * t), s, c);
-    }
+    double t = (double)position * (double)f * 0.63661977236758134;  // 2 / pi: quarter turns
+    t = fma(-4.0, rint(t * 0.25), t);                                 // whole turns off: [-2, 2]
+    const double q = rint(t);
+    const float x = (float)(t - q) * 1.5707963267948966f, x2 = x * x;
+    const int quarter = (int)(float)q;
+    float si = fmaf(x2, 1.f / 362880, -1.f / 5040);
+    si = fmaf(x2, si, 1.f / 120);
+    si = fmaf(x2, si, -1.f / 6);
+    si = fmaf(x * x2, si, x);
+    float co = fmaf(x2, -1.f / 3628800, 1.f / 40320);
+    co = fmaf(x2, co, -1.f / 720);
+    co = fmaf(x2, co, 1.f / 24);
+    co = fmaf(x2, co, -0.5f);
+    co = fmaf(x2, co, 1.f);
+    // turned by `quarter` quarters
+    const float u = quarter & 1 ? si : co, v = quarter & 1 ? co : si;
+    *c = (quarter + 1) & 2 ? -u : u;
+    *s = quarter & 2 ? -v : v;
 }
 
 // The 16 values of a lane as eight pairs (p, q) that a rotation mixes: p and q are the octets a and b, or

@@ -86,7 +86,7 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
 #pragma unroll
             for (int j = 0; j < (MANY ? 8 : 2); ++j) {
                 const int a = MANY ? 8 * sub + j : 2 * lane + j;
-                if (MANY || a < pp.ho * 8) angle_cs<BF16>(pos, pp.inv_freq[a], &c2[j], &s2[j]);
+                if (MANY || a < pp.ho * 8) angle_cs(pos, pp.inv_freq[a], &c2[j], &s2[j]);
             }
         }
         int oa, ob;
@@ -255,7 +255,7 @@ __device__ __forceinline__ void append_heads(AppendRow w, const PrepParams& pp, 
             float c[8], s[8];
             if (rot) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) angle_cs<BF16>(w.pos, pp.inv_freq[sub * 8 + e], &c[e], &s[e]);
+                for (int e = 0; e < 8; ++e) angle_cs(w.pos, pp.inv_freq[sub * 8 + e], &c[e], &s[e]);
             }
             row_coefs<INTER>(coef, kAppendThreads, pp.k_weight, oa, ob, rot, c, s);
         }

@@ -64,9 +64,8 @@ def prep_inputs(T, H, Hkv, dtype, rot, norm, far, seed):
 
 def check_prep(got, x, pos, inv, w, rot, inter, dtype, eps=1e-6):
     """Each value of a pair (or alone) carries the norm's and the rotation's fp32 errors: the sum of squares (16 terms a
-    lane, 3 joins: 20 u), its root, two products, the angle's fraction (pi 2^-25) and sincospi (2 ulp): 40 u of the
-    pair's size together, u = 2^-24; then the rounding to the row's type. For bf16 the sine and cosine are the
-    hardware's, within 2^-21 and the angle's rounding (pi 2^-24) each: 2^-19 of the pair's size."""
+    lane, 3 joins: 20 u), its root, two products, and sine and cosine within 2 u: 40 u of the pair's size together,
+    u = 2^-24; then the rounding to the row's type."""
     y = R.norm_rope(R.f64(x), pos.cpu().numpy(), inv.cpu().numpy(), None if w is None else R.f64(w), rot, inter, eps)
     n = np.array(R.norm_rope(R.f64(x), pos.cpu().numpy(), np.zeros(rot // 2), None if w is None else R.f64(w), rot,
                              inter, eps))
@@ -74,7 +73,7 @@ def check_prep(got, x, pos, inv, w, rot, inter, dtype, eps=1e-6):
     for i in range(rot // 2):
         p, r = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
         size[..., p] = size[..., r] = np.hypot(n[..., p], n[..., r])
-    tol = size * (40 * 2.0 ** -24 + (2.0 ** -19 if dtype == "bf16" else 0))
+    tol = size * 40 * 2.0 ** -24
     tol = tol + (np.abs(y) + tol) * (2 * HALF[dtype]) + 1e-30
     assert np.all(np.abs(R.f64(got) - y) <= tol), np.max(np.abs(R.f64(got) - y) / tol)
 
