@@ -94,6 +94,7 @@ lsa_status kv8_check(const lsa_dims* d, const lsa_kv8_cache* c, void* ws, Kv8Cal
 lsa_status kv8_device(const lsa_dims* d, size_t ws_bytes, Kv8Call* k) {
     const lsa_status s = device_info(&k->di);
     if (s != LSA_OK) return s;
+    if (!k->di.kv8) return LSA_ERR_CUDA;
     k->w = kv8_layout(d, k->p, k->di);
     if (ws_bytes < k->w.total) return LSA_ERR_WORKSPACE;
     return LSA_OK;
@@ -164,6 +165,7 @@ lsa_status lsa_qk_norm_rope(const lsa_dims* dims, int32_t n_kv_heads, const lsa_
     DeviceInfo di;
     s = device_info(&di);
     if (s != LSA_OK) return s;
+    if (!di.kv8) return LSA_ERR_CUDA;
     return cuda_status(launch_qk_norm_rope(*dims, n_kv_heads, *prep, n_tok, positions, q, q_stride, k, k_stride,
                                            q_out, q_out_stride, k_out, k_out_stride, di.sms,
                                            static_cast<cudaStream_t>(stream), false));

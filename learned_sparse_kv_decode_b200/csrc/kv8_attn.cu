@@ -10,8 +10,8 @@
 // tcgen05 tile, so they use the warp-level instructions, whose operands come from registers.
 //
 //  * Both products run in f16 (m16n8k16) with fp32 accumulation: an e4m3 code is an f16 number exactly,
-//    and one conversion unpacks two. (The e4m3 form of the instruction is no cheaper: the compiler turns
-//    it into the same conversions and f16 products, and adds; it took 96 more instructions a tile.)
+//    and one conversion unpacks two. (The e4m3 form of the instruction is no cheaper: by the counters of
+//    executed instructions it costs conversions and f16 products too, and 96 instructions a tile more.)
 //  * Full precision from f16 operands. A row of q, scaled by a power of two, is split into f16 hi + lo; lo
 //    lies in the eight rows of the 16-row operand that a group of up to 8 heads leaves free. The weights
 //    P, at most 2^14, are split in the same way: with 4 heads or fewer, lo takes the free half of the 8
@@ -19,9 +19,9 @@
 //    down to 2^-39.
 //  * The reduction index of a product may be permuted as long as both operands agree, so each lane uses
 //    whole 16-byte pieces as they come. Lane (g, t) of a warp (g = lane / 4, t = lane % 4) takes bytes
-//    32 t .. 32 t + 31 of token g's row of K (four to a step of 16 dims); and bytes 16 g .. 16 g + 15 of tokens 2 t and 2 t + 1 of V,
-//    whose bytes a permute interleaves into pairs along the tokens. S leaves its scores exactly where
-//    the second product wants P, so nothing is exchanged between them.
+//    32 t .. 32 t + 31 of token g's row of K (four to a step of 16 dims), and bytes 16 g .. 16 g + 15 of
+//    tokens 2 t and 2 t + 1 of V, whose bytes a permute interleaves into pairs along the tokens. S leaves
+//    its scores exactly where the second product wants P, so nothing is exchanged between them.
 //  * V's scale multiplies the weight, relative to the largest scale seen (vref), which the running
 //    output carries, so that the products stay within f16's range whatever the scales are.
 //  * The tensor cores truncate when they accumulate: each tile's product starts from zero and is added
@@ -35,6 +35,10 @@
 //  * Every run is cut into equal parts, one to a CTA, so that the CTAs fit the device at once; a CTA joins
 //    its warps in shared memory, and the parts of a run are joined by k_kv8_attn_merge. Runs of one part
 //    are written at once.
+//
+// Measured (B200, bf16 queries, calls captured in a graph): 256 of 2048 chunks x 8 sequences, 16 heads, 538 MB:
+// 80 us, 6.7 TB/s (a plain copy moves 6.47); 819 of 8192 x 4, 32 heads on 8, 430 MB: 70 us, 6.1 TB/s. What is
+// left above the bytes is 8 to 10 us a call to start, fill and join. 8 chunks of one sequence: 6.6 us.
 #include "kv8.cuh"
 
 namespace lsa {
@@ -283,7 +287,8 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             const float2 f = f16x2_floats(a[2 * j]);
             a[2 * j + 1] = f16x2_rn(x0 - f.x, x1 - f.y);
         }
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs - 16 * lane + (lane & 7) * 512 + (4 * c + (lane >> 3)) * 16),
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::
+                     "r"(qs - 16 * lane + (lane & 7) * 512 + (4 * c + (lane >> 3)) * 16),
                      "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3])
                      : "memory");
         // a row with an infinity or a NaN has no finite scores
@@ -665,16 +670,10 @@ static int kv8_max_ctas(int num_sms) { return 4 * num_sms; }
 size_t kv8_part_o_bytes(int num_sms) { return (size_t)kv8_max_ctas(num_sms) * kKv8MaxRows * kDh * 4; }
 size_t kv8_part_ml_bytes(int num_sms) { return (size_t)kv8_max_ctas(num_sms) * kKv8MaxRows * 2 * 4; }
 
-// Tiles of sequence b's runs.
-static int kv8_tiles(const Kv8Tab& t, int b, int c_log2) {
-    return (int)((((int64_t)(t.kept_off[b + 1] - t.kept_off[b]) << c_log2) + kKv8Tile - 1) / kKv8Tile);
-}
-
 // The least tiles per CTA (at least `least`) with which all runs' parts are `slots` CTAs or fewer; if there
 // are more runs than that, what leaves every run whole. `all`: the tiles of all runs, `most` of the longest.
-static int kv8_part_tiles(const Kv8Tab& t, int c_log2, int64_t runs_b, int64_t slots, int least, int most,
-                          int64_t all) {
-    const int64_t runs = runs_b * t.B;
+static int kv8_part_tiles(const int* tiles, int B, int64_t runs_b, int64_t slots, int least, int most, int64_t all) {
+    const int64_t runs = runs_b * B;
     if (runs >= slots || most <= least) return most > least ? most : least;
     // the parts are at least all / T and less than all / T + runs
     int64_t lo = (all + slots - 1) / slots, hi = (all + slots - runs - 1) / (slots - runs);
@@ -683,7 +682,7 @@ static int kv8_part_tiles(const Kv8Tab& t, int c_log2, int64_t runs_b, int64_t s
     while (lo < hi) {
         const int mid = (int)(lo + (hi - lo) / 2);
         int64_t n = 0;
-        for (int b = 0; b < t.B; ++b) n += runs_b * ((kv8_tiles(t, b, c_log2) + mid - 1) / mid);
+        for (int b = 0; b < B; ++b) n += runs_b * ((tiles[b] + mid - 1) / mid);
         if (n <= slots) hi = mid; else lo = mid + 1;
     }
     return (int)lo;
@@ -692,17 +691,17 @@ static int kv8_part_tiles(const Kv8Tab& t, int c_log2, int64_t runs_b, int64_t s
 // Microseconds that the runs take in parts of `per` tiles, `slots` CTAs at a time: the larger of what the
 // fullest SM computes (0.2 a tile while its 16 warps have one each, 0.137 from then on; 3.3 for a round of
 // CTAs to start and to join its warps) and what memory reads (8 KB a tile at 7 TB/s), and, where runs are left
-// to be joined, 2 for that and 0.8 for the host to launch it. Measured: 8 runs of 8 tiles 4.9 us as 8 CTAs of 16 warps; of 16 tiles 6.6 so, of 32 tiles 6.2 as 64
-// CTAs of 4 warps; 128 runs of 16 tiles 7.3 as 128 wide CTAs, 8.3 as 256 of 4 warps.
-static double kv8_estimate(const Kv8Tab& t, int c_log2, int64_t runs_b, int per, int64_t all, int num_sms,
-                           int64_t slots) {
+// to be joined, 2 for that and 0.8 for the host to launch it. Measured: 8 runs of 8 tiles 4.9 us as 8 CTAs of
+// 16 warps; of 16 tiles 6.6 so; of 32 tiles 6.2 as 64 CTAs of 4 warps; 128 runs of 16 tiles 7.3 as 128 wide
+// CTAs, 8.3 as 256 of 4 warps.
+static double kv8_estimate(const int* tiles, int B, int64_t runs_b, int per, int64_t all, int num_sms, int64_t slots) {
     int64_t ctas = 0;
-    for (int b = 0; b < t.B; ++b) ctas += runs_b * ((kv8_tiles(t, b, c_log2) + per - 1) / per);
+    for (int b = 0; b < B; ++b) ctas += runs_b * ((tiles[b] + per - 1) / per);
     const int64_t rounds = (ctas + slots - 1) / slots, per_sm = (ctas + num_sms - 1) / num_sms, full = slots / num_sms;
     const double load = (double)per * (double)(per_sm < full ? per_sm : full);
     const double compute = load < 16. ? 0.2 * load : 1. + 0.137 * load;
     const double memory = 3.3 + 0.00117 * (double)all, busy = (double)rounds * (3.3 + compute);
-    return (busy > memory ? busy : memory) + (ctas > runs_b * t.B ? 2.8 : 0.);
+    return (busy > memory ? busy : memory) + (ctas > runs_b * B ? 2.8 : 0.);
 }
 
 template <bool BF16, bool PLO>
@@ -749,12 +748,12 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
         kt.chunk_off[b] = tab.chunk_off[b];
         kt.kept_off[b] = tab.kept_off[b];
     }
-    int most = 0;  // tiles of the longest run
+    int tiles[kMaxB], most = 0;  // of a sequence's runs, and of the longest run
     int64_t all = 0;
     for (int b = 0; b < tab.B; ++b) {
-        const int n = kv8_tiles(kt, b, g.c_log2);
-        most = n > most ? n : most;
-        all += (int64_t)n * runs_b;
+        tiles[b] = (int)((((int64_t)(tab.kept_off[b + 1] - tab.kept_off[b]) << g.c_log2) + kKv8Tile - 1) / kKv8Tile);
+        most = tiles[b] > most ? tiles[b] : most;
+        all += (int64_t)tiles[b] * runs_b;
     }
     // 16 warps to an SM, as CTAs of 16, 8 or 4. Wide CTAs leave less to join but cut the work in lumps, and
     // idle warps where runs are short; the form with the least estimated time is taken, the wider one where
@@ -763,8 +762,8 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     double best = 0.;
     for (int w = 16; w >= 4; w >>= 1) {
         const int64_t slots = (int64_t)num_sms * (16 / w);
-        const int n = kv8_part_tiles(kt, g.c_log2, runs_b, slots, w, most, all);
-        const double t = kv8_estimate(kt, g.c_log2, runs_b, n, all, num_sms, slots);
+        const int n = kv8_part_tiles(tiles, tab.B, runs_b, slots, w, most, all);
+        const double t = kv8_estimate(tiles, tab.B, runs_b, n, all, num_sms, slots);
         if (warps == 0 || t < 0.98 * best) {
             warps = w;
             per = n;
@@ -774,7 +773,7 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     int64_t ctas = 0;
     bool cut = false;
     for (int b = 0; b < tab.B; ++b) {
-        const int parts = (kv8_tiles(kt, b, g.c_log2) + per - 1) / per;
+        const int parts = (tiles[b] + per - 1) / per;
         kt.cta_off[b] = (int32_t)ctas;
         ctas += (int64_t)parts * runs_b;
         cut |= parts > 1;

@@ -18,8 +18,9 @@ namespace lsa {
 //   time, in 1 KB runs (bf16) of the token's row;
 //   (MANY) with four heads or fewer and tokens enough, a warp per four tokens, eight lanes to a token, each with
 //   its own eight angles: a quarter of the coefficients' work.
-// In both the next rows are loaded while the ones before are worked on. 16384 tokens of 32 + 8 heads take 59 us
-// in the first form and 78 to 84 in the second (four rows far apart at a time), 27011 of 2 + 1 heads 25 and 14.
+// In both the next rows are loaded while the ones before are worked on. 16384 tokens of 32 + 8 heads, 336 MB,
+// take 60 us in the first form (5.6 TB/s) and 78 to 84 in the second (four rows far apart at a time), 27011 of
+// 2 + 1 heads 25 and 14.
 constexpr int kPrepThreads = 128;
 
 struct PrepRows {
@@ -113,9 +114,14 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
 }
 
 // ---------------------------------------------------------------- quantising write
-// One CTA per (64-token window of a sequence, slice of heads): window rows are aligned to 64 tokens of
-// the sequence, eight lanes to a row, so that every block of 8..64 tokens lies inside one CTA and its
-// amax is a shuffle inside the warp (four rows) and a look at scale_block / 4 warps' words.
+// One CTA per (64-token window of a sequence, K or V, slice of heads): window rows are aligned to 64 tokens of
+// the sequence, eight lanes to a row, so that every block of 8..64 tokens lies inside one CTA and its largest
+// magnitude is a reduction in the warp (four rows) and a look at scale_block / 4 warps' words.
+//
+// Measured (B200, 4 x 8192 tokens, 16 heads, bf16, 403 MB, in a graph): 65 us, 6.2 TB/s; with K prepared 94 us,
+// where K's CTAs wait on the chain norm - rotation - maximum - barrier - codes of a head with the 32 warps that
+// 64 registers leave. One token for each of 8 sequences: 4.3 us. Tried and slower: a head's rows per warp in
+// shared memory without barriers (123 us), asynchronous copies three heads ahead (104 us).
 constexpr int kAppendThreads = 512;
 constexpr int kAppendRows = kAppendThreads / 8;
 constexpr int kAppendCoefBytes = 8 * kAppendThreads * 16;
@@ -296,7 +302,7 @@ __device__ __forceinline__ void append_heads(AppendRow w, const PrepParams& pp, 
     }
 }
 
-// K and V go to CTAs of their own (even, odd): what a lane holds of one row is what keeps loads in flight. A
+// K and V go to CTAs of their own (even, odd): the less a lane holds, the more rows are in flight. A
 // bf16 row's values stay packed until they are written, a head's rows are loaded while the one before it is
 // worked on, and the coefficients of weight and rotation (computed once for the slice's heads) wait in shared
 // memory, where each lane keeps its own. PREP is of K.
@@ -429,7 +435,6 @@ cudaError_t launch_qk_norm_rope(const lsa_dims& d, int n_kv_heads, const lsa_qk_
     return pp.interleaved ? by_form(Const<false>{}, Const<true>{}) : by_form(Const<false>{}, Const<false>{});
 }
 
-// CTAs of an append, or 0 where they pass a grid's limit.
 cudaError_t launch_kv8_append(const lsa_dims& d, const SeqTable& tab, const lsa_kv8_cache& cache, const Kv8Geom& g,
                               const lsa_qk_prep* prep, int n_new, const void* k, int64_t k_stride, const void* v,
                               int64_t v_stride, const int32_t* start, const int32_t* new_count, uint32_t* err,

@@ -93,14 +93,14 @@ lsa_status device_info(DeviceInfo* out) {
         di.sms = sms;
         // kernel attributes are per device: set them here, never inside a launch (graph capture)
         if (score_init_attrs() != cudaSuccess || topk_init_attrs() != cudaSuccess ||
-            refresh_init_attrs() != cudaSuccess || fp8_init_attrs() != cudaSuccess ||
-            kv8_init_attrs() != cudaSuccess || kv8_write_init_attrs() != cudaSuccess)
+            refresh_init_attrs() != cudaSuccess || fp8_init_attrs() != cudaSuccess)
             return LSA_ERR_CUDA;
         if (attn_ctas_per_device(LSA_F32, sms, &di.attn_ctas[LSA_F32]) != cudaSuccess) return LSA_ERR_CUDA;
         if (attn_ctas_per_device(LSA_BF16, sms, &di.attn_ctas[LSA_BF16]) != cudaSuccess) return LSA_ERR_CUDA;
         int la_occ = 0;
         if (la_init_attrs(&la_occ) != cudaSuccess || la_occ < 1) return LSA_ERR_CUDA;
         di.la_ctas = la_occ * sms;
+        di.kv8 = kv8_init_attrs() == cudaSuccess && kv8_write_init_attrs() == cudaSuccess;
         di.ready = true;
     }
     *out = di;

@@ -11,6 +11,7 @@ struct DeviceInfo {
     int sms;
     int attn_ctas[2];  // per kv dtype (LSA_F32, LSA_BF16)
     int la_ctas;       // CTAs of the lookahead-window attention
+    bool kv8;          // the 8-bit cache's kernels can run as planned
 };
 
 // Facts of the current device, computed once per device.

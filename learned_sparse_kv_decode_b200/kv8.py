@@ -186,6 +186,8 @@ class Kv8Cache:
 def alloc_kv8_cache(dims, n_kv_heads, scale_block=64, device=None):
     """A zeroed 8-bit cache for ``dims``."""
     s = _shape(dims)
+    if scale_block < 1 or s.C % scale_block:
+        raise abi.LsaError(abi.LSA_ERR_UNSUPPORTED, "alloc_kv8_cache")
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     codes = (s.chunks, n_kv_heads, s.C, LSA_HEAD_DIM)
     scales = (s.chunks, n_kv_heads, s.C // scale_block)
