@@ -581,6 +581,80 @@ def test_calls_on_another_stream(lsa):
     assert torch.equal(a, b)
 
 
+def test_ids_in_any_order_and_twice(lsa):
+    """Kept chunks need not be sorted, and one that is named twice counts twice."""
+    n_b, k_b, C, H, Hkv, sb = [12, 5], [6, 4], 16, 8, 2, 8
+    lens = [190, 70]
+    dims, cache, q = attn_inputs(lsa, n_b, C, H, Hkv, sb, "bf16", lens, "free", 31, k_b)
+    ids = [[11, 3, 3, 0, 11, 7], [4, 4, 4, 4]]
+    ws = lsa.alloc_workspace(dims, kv8=cache)
+    out, lse = torch.empty(2, H, DH, device="cuda"), torch.empty(2, H, device="cuda")
+    lsa.lsa_kv8_decode_attn(dims, cache, q, i32(sum(ids, [])), None, i32(lens), out, lse, ws)
+    check_attn(out, lse, q, cache, n_b, C, ids, lens, H)
+    K, V = (torch.zeros(sum(k_b) * C, Hkv, DH, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lsa.lsa_kv8_gather(dims, cache, i32(sum(ids, [])), i32(lens), K, V, ws)
+    assert torch.equal(K[C:2 * C], K[2 * C:3 * C]) and torch.equal(V[:6 * C][:C], V[4 * C:5 * C])
+    assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
+
+
+def test_offsets_past_32_bits(lsa):
+    """A cache whose codes pass 2^32 bytes: its last chunks written, read back and attended to, as those of a small one."""
+    C, H, Hkv, sb, far = 64, 32, 16, 64, 33000  # 128 KB a chunk: 4.3 GB each of K and V
+    n_b, k_b = [far, 3], [4, 3]
+    dims = make_dims(lsa, n_b, k_b, C, H, "bf16")
+    small = make_dims(lsa, [4, 3], k_b, C, H, "bf16")
+    big, ref = lsa.alloc_kv8_cache(dims, Hkv, sb), lsa.alloc_kv8_cache(small, Hkv, sb)
+    assert big.K8.numel() > 2 ** 32
+    r = np.random.default_rng(6)
+    rows = tensor(r.normal(0, 1, (2, 250, 2 * Hkv, DH)), "bf16")
+    q = tensor(r.normal(0, 1, (2, H, DH)), "bf16")
+    ids, lens = np.arange(4), [4 * C - 1, 150]
+    got = []
+    for d, cache, first in ((dims, big, far - 4), (small, ref, 0)):
+        ws = lsa.alloc_workspace(d, kv8=cache)
+        lsa.lsa_kv8_append(d, cache, None, rows[:, :, :Hkv], rows[:, :, Hkv:], i32([first * C + 5, 1]), i32([250, 149]), ws)
+        di, sl = i32(np.concatenate([first + ids, np.arange(3)])), i32([first * C + lens[0], lens[1]])
+        out, lse = torch.empty(2, H, DH, device="cuda"), torch.empty(2, H, device="cuda")
+        lsa.lsa_kv8_decode_attn(d, cache, q, di, None, sl, out, lse, ws)
+        K, V = (torch.zeros(7 * C, Hkv, DH, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        lsa.lsa_kv8_gather(d, cache, di, sl, K, V, ws)
+        assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
+        got.append((out, lse, K, V, cache.K8[first:].view(torch.uint8), cache.v_scale[first:]))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    check_attn(got[1][0], got[1][1], q, ref, [4, 3], C, [ids, np.arange(3)], lens, H)
+    assert not bool(big.K8.view(torch.uint8)[:far - 4].any())
+
+
+def test_two_streams_at_once(lsa):
+    """Two streams, each with its workspace, over one cache: attention of the one beside the read-back of the other."""
+    n_b, k_b, C, H, Hkv, sb = [400, 300], [300, 300], 64, 8, 8, 64
+    dims, cache, q = attn_inputs(lsa, n_b, C, H, Hkv, sb, "bf16", None, "free", 19, k_b)
+    ids = i32(np.concatenate(kept_ids(n_b, k_b, 5)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wss = [lsa.alloc_workspace(dims, kv8=cache) for _ in range(2)]
+    rows = sum(k_b) * C
+
+    def calls(which, ws):
+        out, lse = torch.empty(2, H, DH, device="cuda"), torch.empty(2, H, device="cuda")
+        K, V = (torch.empty(rows, Hkv, DH, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        for _ in range(5):
+            lsa.lsa_kv8_decode_attn(dims, cache, q * (1 + which), ids if which else None, None, None, out, lse, ws)
+            lsa.lsa_kv8_gather(dims, cache, ids, None, K, V, ws)
+        return out, lse, K, V
+
+    want = [calls(i, wss[0]) for i in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(2):
+        with torch.cuda.stream(streams[i]):
+            got.append(calls(i, wss[i]))
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
 # ---------------------------------------------------------------- the whole step
 def step_inputs(lsa, dtype, H, Hkv, seed, B=3, Q=1):
     r = np.random.default_rng(seed)
