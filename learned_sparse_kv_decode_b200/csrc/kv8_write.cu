@@ -118,14 +118,14 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
 // the sequence, eight lanes to a row, so that every block of 8..64 tokens lies inside one CTA and its largest
 // magnitude is a reduction in the warp (four rows) and a look at scale_block / 4 warps' words.
 //
-// Measured (B200, 4 x 8192 tokens, 16 heads, bf16, 403 MB, in a graph): 65 us, 6.2 TB/s; with K prepared 94 us,
-// where K's CTAs wait on the chain norm - rotation - maximum - barrier - codes of a head with the 32 warps that
-// 64 registers leave. One token for each of 8 sequences: 4.3 us. Tried and slower: a head's rows per warp in
-// shared memory without barriers (123 us), asynchronous copies three heads ahead (104 us).
+// Measured (B200, 16 heads, bf16, in a graph): 4 x 8192 tokens, 403 MB, 65 us, 6.2 TB/s; with K prepared 90 us,
+// 4.5 TB/s, where no one thing binds: the SMs issue in 63% of the cycles, the integer pipe is busy in 54%, and the
+// angles alone cost 4 us, the weights and rotations 13. 4 x 256 tokens prepared 8.6 us; one token for each of
+// 8 sequences 4.7, unprepared 3. Tried and slower (when the whole took 94): a head's rows per warp in shared
+// memory without barriers (123 us), asynchronous copies three heads ahead (104 us).
 constexpr int kAppendThreads = 512;
 constexpr int kAppendRows = kAppendThreads / 8;
 constexpr int kAppendCoefBytes = 8 * kAppendThreads * 16;
-constexpr int kAppendCtas = 16, kAppendPrepCtas = 8;  // CTAs per SM that a long call is cut into
 
 struct AppendParams {
     Kv8Geom g;
@@ -137,6 +137,7 @@ struct AppendParams {
     int32_t n_new;
     int32_t windows;       // per sequence
     int32_t slices, per;   // slices of heads per window, heads per slice
+    uint32_t turn;         // even
 };
 
 // A lane's codes of one row: eight bytes at each of its octets. Usually the scale is 2^e, and multiplying by
@@ -266,23 +267,28 @@ __device__ __forceinline__ void append_heads(AppendRow w, const PrepParams& pp, 
             row_coefs<INTER>(coef, kAppendThreads, pp.k_weight, oa, ob, rot, c, s);
         }
     }
-#pragma unroll 1
+#pragma unroll (BF16 && ALL ? 2 : 1)
     for (int i = 0; i < w.n_h; ++i) {
-        OctetRaw<BF16> xa = na, xb = nb;
-        pa += kRow;
-        pb += kRow;
-        if ((ALL || w.fresh) && i + 1 < w.n_h) {
-            na = octet_load<BF16>(pa, 0);
-            nb = octet_load<BF16>(pb, 0);
-        }
+        OctetRaw<BF16> xa, xb;
+        auto next = [&] {
+            pa += kRow;
+            pb += kRow;
+            if ((ALL || w.fresh) && i + 1 < w.n_h) {
+                na = octet_load<BF16>(pa, 0);
+                nb = octet_load<BF16>(pb, 0);
+            }
+        };
         const float was = !ALL && w.has_old ? *w.scale : 0.f;  // read before the barrier, written after it
         if constexpr (PREP != 0) {
-            RowPairs v = row_pairs<BF16, INTER>(xa, xb);
+            RowPairs v = row_pairs<BF16, INTER>(na, nb);
+            next();
             const float rms = norm ? row_rms(v, eps) : 1.f;
-            if (ALL || w.fresh) {
-                row_apply(v, rms, rot, full, coef, kAppendThreads);
-                row_octets_of<BF16, INTER>(v, &xa, &xb);  // what lsa_qk_norm_rope would have stored
-            }
+            if (ALL || w.fresh) row_apply(v, rms, rot, full, coef, kAppendThreads);
+            row_octets_of<BF16, INTER>(v, &xa, &xb);  // what lsa_qk_norm_rope would have stored
+        } else {
+            xa = na;
+            xb = nb;
+            next();
         }
         uint32_t top = warp_amax<BF16>(xa, xb, err);
         if ((threadIdx.x & 31) == 0) s_amax[i & 1][threadIdx.x >> 5] = top;
@@ -314,7 +320,8 @@ k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uin
     __shared__ uint32_t s_amax[2][kAppendRows / 4];  // [head parity][warp], fp32 bits
     pdl_trigger();
     const int tid = threadIdx.x, r = tid >> 3, warp = tid >> 5, lane = tid & 31;
-    const bool is_v = blockIdx.x & 1;
+    // CTA pairs (c, c ^ 1) are K and V of one cell; which is which alternates (bf16) every `turn` CTAs.
+    const bool is_v = (BF16 ? blockIdx.x ^ blockIdx.x / ap.turn : blockIdx.x) & 1;
     const int cell = blockIdx.x >> 1;
     const int slice = cell % ap.slices, win = cell / ap.slices % ap.windows, b = cell / ap.slices / ap.windows;
 
@@ -346,7 +353,7 @@ k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uin
         const int64_t row_in = (int64_t)b * ap.n_new + (pos - start);
         w.src = (is_v ? ap.v + row_in * ap.v_stride : ap.k + row_in * ap.k_stride) + (int64_t)h0 * kRow;
         // A head's rows are short runs far apart: the slice's heads of a row, which follow one another, are
-        // brought to L2 in one request (99 -> 91 us for the largest prepared append).
+        // brought to L2 in one request (8% of the largest prepared append's time).
         if (w.n_h > 1 && w.fresh && (tid & 7) == 0)
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(w.src), "r"(w.n_h * kRow) : "memory");
         const int within = (int)(pos & ((1 << ap.g.c_log2) - 1));
@@ -455,13 +462,23 @@ cudaError_t launch_kv8_append(const lsa_dims& d, const SeqTable& tab, const lsa_
     ap.n_new = n_new;
     // a run of n tokens touches at most (n + 62) / 64 + 1 aligned windows (one token: one)
     ap.windows = (int)(((int64_t)n_new + 62) / 64 + 1);
-    // Long slices of heads while there are CTAs enough: a row's heads follow one another in memory, and K's
-    // angles are computed once for a slice. Measured on 4 x 8192 tokens, 16 heads, with 4, 8 and 16 CTAs per SM
-    // (K's and V's together): rows that are only quantised 86, 73 and 65 us, prepared rows 105, 91 and 96.
+    // Slices of heads. A row's heads follow one another in memory, and K's angles are computed once for a slice,
+    // so slices are long, but the calls are bound by what an SM works through: as many as make one round of CTAs
+    // (two of bf16 to an SM, of fp32 one; no more than one where that leaves two heads or fewer), and of eight
+    // heads at most, six where nothing is prepared, where there are several rounds. Measured with 16 heads, bf16,
+    // in 1, 2, 3, 4, 8, 16 slices: 4 x 8192 tokens prepared 101, 89, 95, 102, 138, 222 us, not prepared 85, 72,
+    // 65, 69, 90, 139; 4 x 1021 prepared 22.2, 15.3, 19.1, 18.7, 22.6, 32.5; 4 x 256: 21.3, 12.6, 10.4, 9.3,
+    // 10.4, 11.9 (8.7 in 6); 8 x 1, not prepared: 7.9, 5.0, 4.7, 3.7, 3.1, 3.6.
+    const bool bf16 = d.kv_dtype == LSA_BF16;
     const int64_t cells = (int64_t)ap.windows * d.B * 2;
-    const int64_t want = (int64_t)num_sms * (prep != nullptr ? kAppendPrepCtas : kAppendCtas);
-    int64_t slices = cells >= want ? 1 : (want + cells - 1) / cells;
+    const int most = prep != nullptr ? 8 : 6;
+    int64_t slices = num_sms / cells;
+    if (2 * slices < g.Hkv) slices = (bf16 ? 2 : 1) * (int64_t)num_sms / cells;
+    if (slices * most < g.Hkv) slices = (g.Hkv + most - 1) / most;
     if (slices > g.Hkv) slices = g.Hkv;
+    // Two CTAs that share an SM are a round of CTAs apart: one of K and one of V (K's take longer): 15.3 us
+    // instead of 19.7 for 4 x 1021. In fp32 one fits an SM, and this gains nothing (4 x 4096: 87 instead of 84).
+    ap.turn = num_sms & ~1;
     ap.per = (int)((g.Hkv + slices - 1) / slices);
     ap.slices = (g.Hkv + ap.per - 1) / ap.per;
     const int64_t ctas = (int64_t)ap.windows * d.B * ap.slices * 2;
