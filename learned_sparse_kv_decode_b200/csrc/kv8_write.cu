@@ -313,7 +313,7 @@ __device__ __forceinline__ void append_heads(AppendRow w, const PrepParams& pp, 
 // worked on, and the coefficients of weight and rotation (computed once for the slice's heads) wait in shared
 // memory, where each lane keeps its own. PREP is of K.
 template <bool BF16, int PREP>
-__global__ void __launch_bounds__(kAppendThreads, BF16 ? 2 : 1)
+__global__ void __launch_bounds__(kAppendThreads, BF16 || PREP == 0 ? 2 : 1)
 k_kv8_append(const AppendParams ap, const PrepParams pp, const SeqTable tab, uint32_t* err) {
     constexpr int kRow = kDh * (BF16 ? 2 : 4);
     extern __shared__ float4 s_coef[];  // PREP: [8][thread]
@@ -464,16 +464,18 @@ cudaError_t launch_kv8_append(const lsa_dims& d, const SeqTable& tab, const lsa_
     ap.windows = (int)(((int64_t)n_new + 62) / 64 + 1);
     // Slices of heads. A row's heads follow one another in memory, and K's angles are computed once for a slice,
     // so slices are long, but the calls are bound by what an SM works through: as many as make one round of CTAs
-    // (two of bf16 to an SM, of fp32 one; no more than one where that leaves two heads or fewer), and of eight
-    // heads at most, six where nothing is prepared, where there are several rounds. Measured with 16 heads, bf16,
-    // in 1, 2, 3, 4, 8, 16 slices: 4 x 8192 tokens prepared 101, 89, 95, 102, 138, 222 us, not prepared 85, 72,
-    // 65, 69, 90, 139; 4 x 1021 prepared 22.2, 15.3, 19.1, 18.7, 22.6, 32.5; 4 x 256: 21.3, 12.6, 10.4, 9.3,
-    // 10.4, 11.9 (8.7 in 6); 8 x 1, not prepared: 7.9, 5.0, 4.7, 3.7, 3.1, 3.6.
+    // (two to an SM, prepared fp32 one; two rounds of fp32 that is not prepared, whose heads are mostly loads; no
+    // more than one CTA to an SM where that leaves two heads or fewer), and of `most` heads at most where there are
+    // several rounds. Measured with 16 heads, bf16, in 1, 2, 3, 4, 8, 16 slices: 4 x 8192 tokens prepared 101, 89,
+    // 95, 102, 138, 222 us, not prepared 85, 72, 65, 69, 90, 139; 4 x 1021 prepared 22.2, 15.3, 19.1, 18.7, 22.6,
+    // 32.5; 4 x 256: 21.3, 12.6, 10.4, 9.3, 10.4, 11.9 (8.7 in 6); 8 x 1, not prepared: 7.9, 5.0, 4.7, 3.7, 3.1,
+    // 3.6; fp32 4 x 8192, not prepared: 152, 128, 109, 111, 127, 162, 4 x 1021: 30, 23, 25, 22, 21, 25.
     const bool bf16 = d.kv_dtype == LSA_BF16;
     const int64_t cells = (int64_t)ap.windows * d.B * 2;
+    const int64_t round = (int64_t)num_sms * (bf16 ? 2 : prep != nullptr ? 1 : 4);
     const int most = prep != nullptr ? 8 : 6;
     int64_t slices = num_sms / cells;
-    if (2 * slices < g.Hkv) slices = (bf16 ? 2 : 1) * (int64_t)num_sms / cells;
+    if (2 * slices < g.Hkv) slices = round / cells;
     if (slices * most < g.Hkv) slices = (g.Hkv + most - 1) / most;
     if (slices > g.Hkv) slices = g.Hkv;
     // Two CTAs that share an SM are a round of CTAs apart: one of K and one of V (K's take longer): 15.3 us
