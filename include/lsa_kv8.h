@@ -100,7 +100,7 @@ LSA_API lsa_status lsa_kv8_append(const lsa_dims *dims, const lsa_kv8_cache *cac
 /* Read chunks back into resident buffers of the 16- or 32-bit cache's layout (as lsa_gather_kv).
  *   chunk_ids    [sum k_b] int32 local chunk indices, or NULL: every chunk of every sequence in order
  *   K_res, V_res [sum k_b * C][n_kv_heads][Dh] kv_dtype, out ([sum N_b * C] rows if chunk_ids is NULL):
- *                row j*C+t of sequence b's block = code * scale of token ids[j]*C+t, rounded to kv_dtype
+ *                row j*C+t of sequence b's block = code * scale (fp32) of token ids[j]*C+t, rounded to kv_dtype
  * Rows of tokens at or behind seq_len[b], and of ids outside 0..N_b-1 (LSA_ERR_BAD_ID), are left as they
  * were. */
 LSA_API lsa_status lsa_kv8_gather(const lsa_dims *dims, const lsa_kv8_cache *cache, const int32_t *chunk_ids,

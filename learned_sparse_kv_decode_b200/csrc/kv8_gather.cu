@@ -1,5 +1,6 @@
 // kv8_gather.cu - chunks of the 8-bit K/V cache read back into resident buffers of the 16- or 32-bit
-// layout: x = code * scale, one rounding (none for fp32, and for bf16 with power-of-two scales).
+// layout: x = code * scale in fp32 (exact for a power-of-two scale, and then exact in bf16 too), rounded
+// to bf16 where that is the layout's type.
 //
 // Pure streaming: 1 byte read and 2 or 4 written a value. Eight lanes convert a row of 128 codes, 16
 // bytes to a lane; consecutive rows of a CTA are the heads of one token, so that its stores are one

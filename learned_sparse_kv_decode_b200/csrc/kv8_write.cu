@@ -120,8 +120,8 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
 //
 // Measured (B200, 16 heads, bf16, in a graph): 4 x 8192 tokens, 403 MB, 65 us, 6.2 TB/s; with K prepared 90 us,
 // 4.5 TB/s, where no one thing binds: the SMs issue in 63% of the cycles, the integer pipe is busy in 54%, and the
-// angles alone cost 4 us, the weights and rotations 13. 4 x 256 tokens prepared 8.6 us; one token for each of
-// 8 sequences 4.7, unprepared 3. Tried and slower (when the whole took 94): a head's rows per warp in shared
+// angles alone cost 4 us, the weights and rotations 13. fp32: 109 us (6.2 TB/s) and 152. 4 x 256 tokens prepared
+// 8.6 us; one token for each of 8 sequences 4.7, unprepared 3. Tried and slower (when the whole took 94): a head's rows per warp in shared
 // memory without barriers (123 us), asynchronous copies three heads ahead (104 us).
 constexpr int kAppendThreads = 512;
 constexpr int kAppendRows = kAppendThreads / 8;
@@ -431,8 +431,9 @@ cudaError_t launch_qk_norm_rope(const lsa_dims& d, int n_kv_heads, const lsa_qk_
     cfg.blockDim = dim3(kPrepThreads, 1, 1);
     const PrepParams pp = prep_params(&prep);
     auto launch = [&](auto bf, auto inter, auto form) {
-        return cudaLaunchKernelEx(&cfg, k_qk_norm_rope<decltype(bf)::value, decltype(inter)::value, decltype(form)::value>, r,
-                                  pp, positions);
+        return cudaLaunchKernelEx(&cfg,
+                                  k_qk_norm_rope<decltype(bf)::value, decltype(inter)::value, decltype(form)::value>,
+                                  r, pp, positions);
     };
     auto by_form = [&](auto bf, auto inter) {
         return many ? launch(bf, inter, Const<true>{}) : launch(bf, inter, Const<false>{});
@@ -480,7 +481,7 @@ cudaError_t launch_kv8_append(const lsa_dims& d, const SeqTable& tab, const lsa_
     if (slices > g.Hkv) slices = g.Hkv;
     // Two CTAs that share an SM are a round of CTAs apart: one of K and one of V (K's take longer): 15.3 us
     // instead of 19.7 for 4 x 1021. In fp32 one fits an SM, and this gains nothing (4 x 4096: 87 instead of 84).
-    ap.turn = num_sms & ~1;
+    ap.turn = num_sms > 1 ? num_sms & ~1 : 2;
     ap.per = (int)((g.Hkv + slices - 1) / slices);
     ap.slices = (g.Hkv + ap.per - 1) / ap.per;
     const int64_t ctas = (int64_t)ap.windows * d.B * ap.slices * 2;
