@@ -37,8 +37,11 @@
 //    are written at once.
 //
 // Measured (B200, bf16 queries, calls captured in a graph): 256 of 2048 chunks x 8 sequences, 16 heads, 538 MB:
-// 80 us, 6.7 TB/s (a plain copy moves 6.47); 819 of 8192 x 4, 32 heads on 8, 430 MB: 70 us, 6.1 TB/s. What is
-// left above the bytes is 8 to 10 us a call to start, fill and join. 8 chunks of one sequence: 6.6 us.
+// 81 us, 6.6 TB/s (a plain copy moves 6.47); 819 of 8192 x 4, 32 heads on 8, 430 MB: 70 us, 6.1 TB/s. What is
+// left above the bytes is 8 to 10 us a call to start, fill and join. 32 ragged sequences with groups of 8, 355 MB:
+// 67 us, 5.3 TB/s. 8 chunks of one sequence: 6.7 us.
+#include <algorithm>
+
 #include "kv8.cuh"
 
 namespace lsa {
@@ -60,8 +63,10 @@ struct Kv8Tab {
     int32_t B;
     int32_t chunk_off[kMaxB + 1];
     int32_t kept_off[kMaxB + 1];
-    int32_t cta_off[kMaxB + 1];
+    int32_t cta_off[kMaxB + 1];  // by place: sequences ordered by the length of their parts, longest first
+    uint8_t seq_at[kMaxB], place_of[kMaxB];
 };
+static_assert(kMaxB <= 256, "places fit in a byte");
 
 struct Kv8AttnParams {
     Kv8Geom g;
@@ -74,6 +79,7 @@ struct Kv8AttnParams {
     int32_t rts;        // runs per K/V head: group / rows
     int32_t runs_log2;  // log2 of a sequence's runs, Hkv * rts
     int32_t len_add;    // added to seq_len
+    int32_t num_sms;
     float qscale;       // log2(e) / sqrt(Dh)
 };
 
@@ -125,14 +131,24 @@ __device__ __forceinline__ uint4 kv8_lds16(uint32_t addr) {
     return v;
 }
 
-// The sequence whose CTAs hold CTA c.
-__device__ __forceinline__ int kv8_seq_of(const Kv8Tab& tab, int c) {
+// The place of the sequence whose CTAs hold CTA c.
+__device__ __forceinline__ int kv8_place_of(const Kv8Tab& tab, int c) {
     int lo = 0, hi = tab.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (tab.cta_off[mid] <= c) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// The part that a CTA takes. Of the CTAs that share an SM from the start (a round apart), every other full round
+// is turned about, so that long parts (they come first) meet short ones. 32 ragged sequences, 4 runs each: 71 -> 67
+// us; 250: 70 -> 63.
+template <int WARPS>
+__device__ __forceinline__ int kv8_cta(int num_sms) {
+    const int c = blockIdx.x, round = c / num_sms;
+    const bool turned = (round & 1) && round < 16 / WARPS && (round + 1) * num_sms <= (int)gridDim.x;
+    return turned ? (2 * round + 1) * num_sms - 1 - c : c;
 }
 
 // Grid: all parts of all runs; WARPS * 32 threads. BF16: the type of q; PLO: groups of 8 (a second product
@@ -146,11 +162,18 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     pdl_trigger();
 
     // ---- this CTA's part: a sequence's CTAs are ordered by part, then run
-    const int b = kv8_seq_of(tab, blockIdx.x);
-    const int idx = blockIdx.x - tab.cta_off[b], run = idx & ((1 << p.runs_log2) - 1), part = idx >> p.runs_log2;
-    const int parts = (tab.cta_off[b + 1] - tab.cta_off[b]) >> p.runs_log2;
+    const int cta = kv8_cta<WARPS>(p.num_sms);
+    const int place = kv8_place_of(tab, cta), b = tab.seq_at[place];
+    const int idx = cta - tab.cta_off[place], run = idx & ((1 << p.runs_log2) - 1), part = idx >> p.runs_log2;
+    const int parts = (tab.cta_off[place + 1] - tab.cta_off[place]) >> p.runs_log2;
     const int h = run / p.rts;
     const int qrow0 = b * p.H + run * p.rows;
+    __shared__ int s_part[3];  // for the end: registers are short in between
+    if (tid == 0) {
+        s_part[0] = cta;
+        s_part[1] = parts;
+        s_part[2] = qrow0;
+    }
     int tile0, tile1;
     {
         const int tokens = (tab.kept_off[b + 1] - tab.kept_off[b]) << c_log2;
@@ -476,6 +499,7 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     }
     cp_async_wait<0>();
     __syncthreads();  // the tiles are done with
+    const int my_cta = s_part[0], my_parts = s_part[1], my_row = s_part[2];
     if (t == 0 && g < p.rows) {
         s_ml[warp][g][0] = m == -INFINITY ? -INFINITY : m - kKv8PShift;
         s_ml[warp][g][1] = l;
@@ -536,13 +560,13 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             A.x = fmaf(f, v.x, A.x); A.y = fmaf(f, v.y, A.y);
             A.z = fmaf(f, v.z, A.z); A.w = fmaf(f, v.w, A.w);
         }
-        if (parts == 1) {
-            *reinterpret_cast<float4*>(p.out + (int64_t)(qrow0 + r) * kDh + d) =
+        if (my_parts == 1) {
+            *reinterpret_cast<float4*>(p.out + (int64_t)(my_row + r) * kDh + d) =
                 L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(A.x / L, A.y / L, A.z / L, A.w / L);
             if (d == 0 && p.lse != nullptr)
-                p.lse[qrow0 + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+                p.lse[my_row + r] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
         } else {
-            const int64_t at = (int64_t)blockIdx.x * kKv8MaxRows + r;
+            const int64_t at = (int64_t)my_cta * kKv8MaxRows + r;
             *reinterpret_cast<float4*>(p.part_o + at * kDh + d) = A;
             if (d == 0) {
                 p.part_ml[at * 2] = M;
@@ -564,8 +588,9 @@ k_kv8_attn_merge(const Kv8AttnParams p, const Kv8Tab tab, int wpr) {
     const int b = r / p.H, run = (r - b * p.H) / p.rows, row = r & (p.rows - 1);
     int parts = 0, cta = 0;
     if (b < tab.B) {
-        parts = (tab.cta_off[b + 1] - tab.cta_off[b]) >> p.runs_log2;
-        cta = tab.cta_off[b] + run;
+        const int place = tab.place_of[b];
+        parts = (tab.cta_off[place + 1] - tab.cta_off[place]) >> p.runs_log2;
+        cta = tab.cta_off[place] + run;
     }
     pdl_wait();
     // parts == 1: written by the CTA that held the run
@@ -740,6 +765,7 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
     const int runs_b = g.Hkv * p.rts;
     while ((1 << p.runs_log2) < runs_b) ++p.runs_log2;
     p.len_add = len_add;
+    p.num_sms = num_sms;
     p.qscale = 1.4426950408889634f / sqrtf((float)kDh);
 
     Kv8Tab kt;
@@ -770,11 +796,22 @@ cudaError_t launch_kv8_attn(const lsa_dims& d, const SeqTable& tab, const lsa_kv
             best = t;
         }
     }
-    int64_t ctas = 0;
-    bool cut = false;
+    // Places: the sequences by the length of their longest parts, longest first.
+    int part_len[kMaxB], order[kMaxB];
     for (int b = 0; b < tab.B; ++b) {
         const int parts = (tiles[b] + per - 1) / per;
-        kt.cta_off[b] = (int32_t)ctas;
+        part_len[b] = (tiles[b] + parts - 1) / parts;
+        order[b] = b;
+    }
+    std::sort(order, order + tab.B,
+              [&](int x, int y) { return part_len[x] > part_len[y] || (part_len[x] == part_len[y] && x < y); });
+    int64_t ctas = 0;
+    bool cut = false;
+    for (int i = 0; i < tab.B; ++i) {
+        const int b = order[i], parts = (tiles[b] + per - 1) / per;
+        kt.seq_at[i] = (uint8_t)b;
+        kt.place_of[b] = (uint8_t)i;
+        kt.cta_off[i] = (int32_t)ctas;
         ctas += (int64_t)parts * runs_b;
         cut |= parts > 1;
     }
