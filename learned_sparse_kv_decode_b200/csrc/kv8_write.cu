@@ -119,7 +119,7 @@ k_qk_norm_rope(const PrepRows r, const PrepParams pp, const int32_t* __restrict_
 // magnitude is a reduction in the warp (four rows) and a look at scale_block / 4 warps' words.
 //
 // Measured (B200, 16 heads, bf16, in a graph): 4 x 8192 tokens, 403 MB, 65 us, 6.2 TB/s; with K prepared 90 us,
-// 4.5 TB/s, where no one thing binds: the SMs issue in 63% of the cycles, the integer pipe is busy in 54%, and the
+// 4.5 TB/s, where no one thing binds: the SMs issue in 62% of the cycles, the integer pipe is busy in 51%, and the
 // angles alone cost 4 us, the weights and rotations 13. fp32: 109 us (6.2 TB/s) and 152. 4 x 256 tokens prepared
 // 8.6 us; one token for each of 8 sequences 4.7, unprepared 3. Tried and slower (when the whole took 94): a head's rows per warp in shared
 // memory without barriers (123 us), asynchronous copies three heads ahead (104 us).
