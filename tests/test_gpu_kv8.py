@@ -308,6 +308,33 @@ def test_append_prepares_as_the_separate_call(lsa, dtype, rot, inter, norm, n):
     assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
 
 
+@pytest.mark.parametrize("dtype,B,n", [("bf16", 4, 700), ("f32", 4, 700), ("bf16", 32, 200), ("f32", 32, 200)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_of_many_rows_walks_several_heads(lsa, dtype, B, n, inter):
+    """Calls long enough that a CTA takes three to eight heads one after the other: plain rows against the definition,
+    prepared rows bit for bit against the two separate calls."""
+    C, Hkv, sb = 64, 16, 32
+    n_b = [n // C + 2 + b % 3 for b in range(B)]
+    starts, counts = [(29 * b) % 65 for b in range(B)], [n - 13 * (b % 4) for b in range(B)]
+    dims, t, k, v = append_case(lsa, n_b, C, Hkv, sb, dtype, n, 50 + B, 1.5)
+    caches = [{m: x.clone() for m, x in t.items()} for _ in range(3)]
+    ca, cb, cc = (lsa.Kv8Cache(dims, Hkv, sb, y["K8"], y["V8"], y["k_scale"], y["v_scale"]) for y in caches)
+    ws = lsa.alloc_workspace(dims, kv8=ca)
+    lsa.lsa_kv8_append(dims, ca, None, k, v, i32(starts), i32(counts), ws)
+    check_append(t, caches[0], R.f64(k), n_b, C, sb, starts, counts, "K")
+    check_append(t, caches[0], R.f64(v), n_b, C, sb, starts, counts, "V")
+    _, _, inv, w = prep_inputs(1, 1, 1, dtype, 128, True, 2, 14)
+    prep = lsa.QkPrep(128, inv, None, w[1], 1e-5, inter)
+    lsa.lsa_kv8_append(dims, cb, prep, k, v, i32(starts), i32(counts), ws)
+    pos = (torch.tensor(starts)[:, None] + torch.arange(n)).to(torch.int32).cuda()
+    kp = torch.empty((B, n, Hkv, DH), dtype=k.dtype, device="cuda")
+    lsa.lsa_qk_norm_rope(dims, prep, pos.view(-1), None, k.contiguous().view(-1, Hkv, DH), None, kp.view(-1, Hkv, DH))
+    lsa.lsa_kv8_append(dims, cc, None, kp, v, i32(starts), i32(counts), ws)
+    for m in t:
+        assert torch.equal(caches[1][m].view(torch.uint8), caches[2][m].view(torch.uint8)), m
+    assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
+
+
 # ---------------------------------------------------------------- reading back
 GATHER = [
     # n_b, k_b, C, Hkv, sb, dtype, lengths
