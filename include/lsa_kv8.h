@@ -115,7 +115,8 @@ LSA_API lsa_status lsa_kv8_gather(const lsa_dims *dims, const lsa_kv8_cache *cac
  *   kept_count [B] int32 device or NULL: attend over the first kept_count[b] ids only (with chunk_ids NULL,
  *              over the first kept_count[b] chunks)
  *   out        [B][H][Dh] float32;  lse [B][H] float32 natural-log sum of exp of the scaled logits, or NULL
- * A sequence with no token to attend to gets out = 0 and lse = -inf. fp32 softmax and sums; the codes are
+ * A sequence with no token to attend to gets out = 0 and lse = -inf; a head with a NaN or an infinity in its q
+ * gets NaN. fp32 softmax and sums; the codes are
  * multiplied exactly (as f16) with q and the softmax weights, both held as the sum of two f16 numbers. */
 LSA_API lsa_status lsa_kv8_decode_attn(const lsa_dims *dims, const lsa_kv8_cache *cache, const void *q,
                                        const int32_t *chunk_ids, const int32_t *kept_count,

@@ -569,7 +569,9 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
             const int64_t at = (int64_t)my_cta * kKv8MaxRows + r;
             *reinterpret_cast<float4*>(p.part_o + at * kDh + d) = A;
             if (d == 0) {
-                p.part_ml[at * 2] = M;
+                // The join takes a maximum of -inf for a part without tokens. Scores that are all NaN leave it so
+                // too (a maximum passes NaN over), with a sum that is NaN: any finite maximum carries that on.
+                p.part_ml[at * 2] = M == -INFINITY && L != 0.f ? 0.f : M;
                 p.part_ml[at * 2 + 1] = L;
             }
         }
