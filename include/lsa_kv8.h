@@ -116,8 +116,10 @@ LSA_API lsa_status lsa_kv8_gather(const lsa_dims *dims, const lsa_kv8_cache *cac
  *              over the first kept_count[b] chunks)
  *   out        [B][H][Dh] float32;  lse [B][H] float32 natural-log sum of exp of the scaled logits, or NULL
  * A sequence with no token to attend to gets out = 0 and lse = -inf; a head with a NaN or an infinity in its q
- * gets NaN. fp32 softmax and sums; the codes are
- * multiplied exactly (as f16) with q and the softmax weights, both held as the sum of two f16 numbers. */
+ * gets NaN. fp32 softmax and sums; the codes are multiplied exactly (as f16) with q and with the softmax
+ * weights times V's scales, both held as the sum of two f16 numbers. That is 22 bits, for q down to 2^-17 of
+ * its row's largest value, for a weight times its scale down to 2^-16 of the head's largest such product (an
+ * error of 2^-38 of the largest below that). A weight below 2^-126 of the largest counts as 0. */
 LSA_API lsa_status lsa_kv8_decode_attn(const lsa_dims *dims, const lsa_kv8_cache *cache, const void *q,
                                        const int32_t *chunk_ids, const int32_t *kept_count,
                                        const int32_t *seq_len, float *out, float *lse, void *ws, size_t ws_bytes,

@@ -14,16 +14,18 @@
 //    executed instructions it costs conversions and f16 products too, and 96 instructions a tile more.)
 //  * Full precision from f16 operands. A row of q, scaled by a power of two, is split into f16 hi + lo; lo
 //    lies in the eight rows of the 16-row operand that a group of up to 8 heads leaves free. The weights
-//    P, at most 2^14, are split in the same way: with 4 heads or fewer, lo takes the free half of the 8
-//    columns, with 8 heads a second product. Weights keep 22 bits down to 2^-28 of the largest and reach
-//    down to 2^-39.
+//    P are split in the same way: with 4 heads or fewer, lo takes the free half of the 8 columns, with 8
+//    heads a second product.
 //  * The reduction index of a product may be permuted as long as both operands agree, so each lane uses
 //    whole 16-byte pieces as they come. Lane (g, t) of a warp (g = lane / 4, t = lane % 4) takes bytes
 //    32 t .. 32 t + 31 of token g's row of K (four to a step of 16 dims), and bytes 16 g .. 16 g + 15 of
 //    tokens 2 t and 2 t + 1 of V, whose bytes a permute interleaves into pairs along the tokens. S leaves
 //    its scores exactly where the second product wants P, so nothing is exchanged between them.
-//  * V's scale multiplies the weight, relative to the largest scale seen (vref), which the running
-//    output carries, so that the products stay within f16's range whatever the scales are.
+//  * V's scale multiplies the weight, times a power of two that brings the largest such product that the
+//    row has met to 2^13..2^15, so that they fit f16 whatever the scales are; the running output carries
+//    that power of two. A product keeps 22 bits down to 2^-16 of the row's largest, and what is below
+//    2^-38 of it is lost, as it would be in an fp32 sum. (A power of two for all rows, from the scales
+//    alone, would let a block of large scale that a row hardly attends to take that row's bits.)
 //  * The tensor cores truncate when they accumulate: each tile's product starts from zero and is added
 //    to the running output in fp32, rounded to nearest, by the multiply-add that also rescales it.
 //  * A warp streams tiles of 32 tokens of one (sequence, K/V head) run through its own 4 KB of K and 4 KB
@@ -49,10 +51,11 @@ namespace lsa {
 constexpr int kKv8Tile = 32;       // tokens per tile: 4 octets
 constexpr int kKv8Batch = 8;       // tiles whose 32 octets the lanes hold
 constexpr int kKv8MaxRows = 8;     // query heads per run
-constexpr float kKv8PShift = 14.f; // weights are at most 2^14
+constexpr float kKv8Top = 14.f;    // weights times V's scales are brought to about 2^14
+constexpr float kKv8MinD = -112.f; // and the factor for that stays within fp32
 constexpr int kKv8SlotV = kKv8Tile * kDh;          // a warp's shared memory: K rows, V rows,
-constexpr int kKv8Meta = 2 * kKv8Tile * kDh;       // two batches of ks[32], vs / vref [32], n[32]
-constexpr int kKv8MetaBytes = 3 * 32 * 4;
+constexpr int kKv8Meta = 2 * kKv8Tile * kDh;       // two batches of ks[32], vs[32], n[32], vs's exponents[32]
+constexpr int kKv8MetaBytes = 4 * 32 * 4;
 constexpr int kKv8WarpBytes = kKv8Meta + 2 * kKv8MetaBytes;
 constexpr int kKv8JoinBytes = kKv8MaxRows * (kDh + 2) * 4;  // of a warp; takes the tiles' place
 static_assert(kKv8JoinBytes <= kKv8WarpBytes, "the join's buffers lie where the tiles were");
@@ -87,6 +90,20 @@ struct Kv8AttnParams {
 __device__ __forceinline__ float kv8_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// log2 of the power of two that brings 2^d, or a little less, to 2^14: an integer that fits the low bits
+// of the sum, rounded down (a whole one may be 1 less).
+__device__ __forceinline__ float kv8_up(float d) { return (kKv8Top - 0.5f - d) + 12582912.f; }
+// That power of two (sign 1) or its inverse (-1).
+__device__ __forceinline__ float kv8_pow2(float up, int sign) {
+    return __uint_as_float((127u << 23) + (uint32_t)sign * (__float_as_uint(up) << 23));
+}
+// x, the largest finite number in place of an infinity; NaN stays.
+__device__ __forceinline__ float kv8_finite(float x) {
+    float y;
+    asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -322,8 +339,11 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     __syncthreads();
     const float qmul = s_qmul[g];
 
-    float o[8][4], m = -INFINITY, l = 0.f, vref = 0.f;
+    // of the lane's row: running maximum and sum, and log2 of its largest weight times a V scale (the scale's
+    // power of two) relative to that maximum
+    float o[8][4], m = -INFINITY, l = 0.f, d = kKv8MinD;
     const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool one = p.g.sb_log2 >= 5;  // a tile lies in one block
     uint32_t full = 0;  // octets of the batch in use whose 8 tokens all take part
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -333,18 +353,9 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         const uint32_t mt = meta + (it & kKv8Batch ? kKv8MetaBytes : 0);  // this batch's, at this lane
         cp_async_wait<1>();
         __syncwarp();  // every lane's copies of K have landed
-        float vf = 1.f;
-        if (l0 == 0) {  // a new batch: its scales, and V's reference, which it may raise
+        if (l0 == 0) {  // a new batch
             full = __ballot_sync(0xffffffffu, kv8_lds(mt + 256) == 8);
-            const float vs = __uint_as_float(kv8_lds(mt + 128));
-            float vtop = vs;
-#pragma unroll
-            for (int k = 1; k < 32; k <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, k));
-            if (vtop > vref && vtop >= 1.17549435e-38f) {
-                vf = vref / vtop;
-                vref = vtop;
-            }
-            kv8_sts(mt + 128, vref > 0.f ? vs / vref : 0.f);  // read behind the next barrier
+            kv8_sts(mt + 384, (float)((int)(kv8_lds(mt + 128) >> 23) - 127));  // read behind the next barrier
         }
         const bool whole = (full >> l0 & 15u) == 15u;
         const uint32_t mb = mt - 4 * lane + 4 * l0;  // of the tile's four octets
@@ -396,29 +407,50 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
         if ((it + 1) % kKv8Batch == 0) next_batch(it + 1);
         copy(it + 1, p.K8, 0);
 
-        // ---- running maximum of the lane's row of q
-        float mx = m;
+        // ---- running maximum of the lane's row of q, with and without V's scales
+        float two[4], mx, mv;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, sc[i]);
+        for (int i = 0; i < 4; ++i) two[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
+        mx = fmaxf(fmaxf(two[0], two[1]), fmaxf(two[2], two[3]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        const float al = kv8_ex2(m - ref);
+        if (one) {
+            mv = mx + __uint_as_float(kv8_lds(mb + 384));
+        } else {
+            const uint4 e4 = kv8_lds16(mb + 384);
+            mv = fmaxf(fmaxf(two[0] + __uint_as_float(e4.x), two[1] + __uint_as_float(e4.y)),
+                       fmaxf(two[2] + __uint_as_float(e4.z), two[3] + __uint_as_float(e4.w)));
+            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 1));
+            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, 2));
+        }
+        mx = fmaxf(mx, m);
+        const float ref = mx == -INFINITY ? 0.f : mx, dm = m - ref;
+        const float was = kv8_up(d);
+        d = fmaxf(fmaxf(d + dm, mv - ref), kKv8MinD);
+        const float up = kv8_up(d);
+        const float al = kv8_ex2(dm), ao = kv8_ex2(dm + (up - was));
         m = mx;
-        const float a0 = __shfl_sync(0xffffffffu, al, 8 * t) * vf;  // of columns 2 t and 2 t + 1
-        const float a1 = __shfl_sync(0xffffffffu, al, 8 * t + 4) * vf;
-        // ---- weights (times 2^14, which out = O / l cancels) and their f16 halves
-        const float ms = ref - kKv8PShift;
+        const float a0 = __shfl_sync(0xffffffffu, ao, 8 * t);  // of columns 2 t and 2 t + 1
+        const float a1 = __shfl_sync(0xffffffffu, ao, 8 * t + 4);
+        // ---- weights, and the f16 halves of their products with V's scales
         uint32_t ph[4], pl[PLO ? 4 : 1];
         {
+            // a scale that leaves fp32 here is one of weights below 2^-100
+            const float c = kv8_pow2(up, 1);
             const uint4 r4 = kv8_lds16(mb + 128);
-            const uint32_t rv[4] = {r4.x, r4.y, r4.z, r4.w};
+            float v[4];
+            v[0] = v[1] = v[2] = v[3] = kv8_finite(__uint_as_float(r4.x) * c);
+            if (!one) {
+                v[1] = kv8_finite(__uint_as_float(r4.y) * c);
+                v[2] = kv8_finite(__uint_as_float(r4.z) * c);
+                v[3] = kv8_finite(__uint_as_float(r4.w) * c);
+            }
             float ls = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float p0 = kv8_ex2(sc[2 * i] - ms), p1 = kv8_ex2(sc[2 * i + 1] - ms);
+                const float p0 = kv8_ex2(sc[2 * i] - ref), p1 = kv8_ex2(sc[2 * i + 1] - ref);
                 ls += p0 + p1;
-                const float w0 = p0 * __uint_as_float(rv[i]), w1 = p1 * __uint_as_float(rv[i]);
+                const float w0 = p0 * v[i], w1 = p1 * v[i];
                 ph[i] = f16x2_rn(w0, w1);
                 const float2 f = f16x2_floats(ph[i]);
                 const uint32_t low = f16x2_rn(w0 - f.x, w1 - f.y);
@@ -491,6 +523,8 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     float(*s_ml)[kKv8MaxRows][2] = reinterpret_cast<float(*)[kKv8MaxRows][2]>(smem + WARPS * kKv8MaxRows * kDh * 4);
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const float down = kv8_pow2(kv8_up(d), -1);  // of the lane's row; of columns 2 t and 2 t + 1:
+    const float downs[2] = {__shfl_sync(0xffffffffu, down, 8 * t), __shfl_sync(0xffffffffu, down, 8 * t + 4)};
     if constexpr (!PLO) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -501,7 +535,7 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
     __syncthreads();  // the tiles are done with
     const int my_cta = s_part[0], my_parts = s_part[1], my_row = s_part[2];
     if (t == 0 && g < p.rows) {
-        s_ml[warp][g][0] = m == -INFINITY ? -INFINITY : m - kKv8PShift;
+        s_ml[warp][g][0] = m;
         s_ml[warp][g][1] = l;
     }
 #pragma unroll
@@ -511,8 +545,8 @@ k_kv8_attn(const Kv8AttnParams p, const Kv8Tab tab, uint32_t* err) {
 #pragma unroll
             for (int w = 0; w < 4; ++w)
                 *reinterpret_cast<float4*>(&s_o[warp][r][16 * g + 4 * w]) =
-                    make_float4(o[2 * w][e] * vref, o[2 * w][2 + e] * vref, o[2 * w + 1][e] * vref,
-                                o[2 * w + 1][2 + e] * vref);
+                    make_float4(o[2 * w][e] * downs[e], o[2 * w][2 + e] * downs[e], o[2 * w + 1][e] * downs[e],
+                                o[2 * w + 1][2 + e] * downs[e]);
         }
     }
     __syncthreads();

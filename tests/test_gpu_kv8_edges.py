@@ -1,11 +1,11 @@
 """GPU tests of the 8-bit K/V cache at values and sizes where a kernel's own number format, split or plan could show:
-non-finite queries."""
+non-finite queries, V scales of very unlike size."""
 import numpy as np
 import pytest
 import torch
 
 from tests import _kv8 as R
-from tests.test_gpu_kv8 import attn_inputs, i32
+from tests.test_gpu_kv8 import attn_inputs, i32, make_dims, tensor
 
 pytestmark = pytest.mark.gpu
 DH = R.DH
@@ -59,3 +59,111 @@ def test_keys_that_are_nan_over_whole_parts_make_their_head_nan(lsa, H, Hkv):
         cache.K8.view(torch.uint8)[a:, 1] = 0x7F
         lsa.lsa_kv8_decode_attn(dims, cache, q, None, None, None, out, None, ws)
         assert bool(torch.isnan(out[0, g:]).all()) and torch.equal(out[0, :g], out0[0, :g]), a
+
+
+# ---------------------------------------------------------------- V's scales
+def attention_and_bounds(q, K, V, ks, vs):
+    """One sequence over all its tokens in 64 bits. q [H][128]; K, V code values [n][Hkv][C][128]; scales
+    [n][Hkv][C/sb]. -> out, lse and their bounds, out's for each value.
+
+    With u = 2^-24 and p the normalised weights: a logit is off by delta = 2^-18 (A_t + A_max), A_t = sum |q k| / sqrt(128)
+    of its token and A_max of the one with the largest logit (q's halves 2^-22 of sum |q k|, fp32 sums that truncate
+    2^-20, scales and differences 4 u), which changes p_t v_t in the sum over tokens and p_t in the one that divides it.
+    Weights, their f16 halves and the joins: 2^-20 each at most, 2^-18 together. Sums with truncation: 2^-23 for each
+    of at most n / 16 steps, and 64 for the joins, in both sums. All of these are relative to sum p |v| of the value's
+    own column. What is not: the low f16 half ends at 2^-24, half a step of it is 2^-25, and products p vs are brought
+    to 2^13 at least, so a token's is off by up to 2^-38 of the largest, times a code of up to 448. And a weight below
+    2^-125 of the largest may count as 0."""
+    H, Hkv, C = q.shape[0], K.shape[1], K.shape[2]
+    sb = C // ks.shape[2]
+    out, lse, tol, tol_l = np.zeros((H, DH)), np.zeros(H), np.zeros((H, DH)), np.zeros(H)
+    for h in range(H):
+        kv = h // (H // Hkv)
+        s = np.repeat(vs[:, kv], sb, -1).reshape(-1)
+        k = K[:, kv].reshape(-1, DH) * np.repeat(ks[:, kv], sb, -1).reshape(-1, 1)
+        v = V[:, kv].reshape(-1, DH) * s[:, None]
+        n = len(k)
+        logit = k @ q[h] / np.sqrt(DH)
+        A = np.abs(k) @ np.abs(q[h]) / np.sqrt(DH)
+        top = logit.argmax()
+        p = np.exp(logit - logit[top])
+        total = p.sum()
+        lse[h], p = logit[top] + np.log(total), p / total
+        out[h], size = p @ v, p @ np.abs(v)
+        delta = np.expm1(2.0 ** -18 * (A + A[top]))
+        steps = (n / 16 + 64) * 2.0 ** -23
+        lost = p < 2.0 ** -125 * p[top]
+        tol[h] = ((p * delta) @ np.abs(v) + size * (p @ delta) + size * (2.0 ** -18 + 2 * steps)
+                  + n * 2.0 ** -38 * 448 * (p * s).max() + p[lost] @ np.abs(v[lost]))
+        tol_l[h] = p @ delta + 2.0 ** -18 * (1 + A[top]) + steps + 2.0 ** -22 * abs(lse[h])
+    return out, lse, tol, tol_l
+
+
+def scaled_cache(lsa, n, C, H, Hkv, sb, dtype, exponents, seed, low=()):
+    """One sequence whose K are N(0, 1) and whose V codes are random, with V's scales 2^exponents [n][Hkv][C/sb]. The keys
+    of the chunks `low`, {chunk: logit}, give about that logit with the queries, which are multiples of one row."""
+    r = np.random.default_rng(seed)
+    dims = make_dims(lsa, [n], [n], C, H, dtype)
+    base = r.normal(0, 1.5, DH)
+    q = tensor((base * (1 + 0.01 * np.arange(H))[:, None])[None], dtype)
+    K = r.normal(0, 1, (n, Hkv, C, DH))
+    for c, logit in dict(low).items():
+        K[c] = base * (logit * np.sqrt(DH) / (base @ base)) * r.uniform(0.97, 1.03, (Hkv, C, 1))
+    ks = np.exp2(np.ceil(np.log2(np.maximum(np.abs(K).reshape(n, Hkv, C // sb, -1).max(-1), 1e-3) / 448)))
+    k8 = torch.from_numpy(K / np.repeat(ks, sb, -1)[..., None]).float().cuda().to(torch.float8_e4m3fn)
+    c = r.integers(0, 256, (n, Hkv, C, DH), dtype=np.uint8)
+    c[(c & 127) == 127] = 0x30
+    f32 = [torch.from_numpy(x.astype(np.float32)).cuda() for x in (ks, np.exp2(exponents))]
+    cache = lsa.Kv8Cache(dims, Hkv, sb, k8, torch.from_numpy(c).cuda(), *f32)
+    return dims, cache, q
+
+
+def check_scaled(lsa, dims, cache, q, ids=None, chunks=None):
+    H = q.shape[1]
+    out, lse = torch.empty(1, H, DH, device="cuda"), torch.empty(1, H, device="cuda")
+    ws = lsa.alloc_workspace(dims, kv8=cache)
+    lsa.lsa_kv8_decode_attn(dims, cache, q, None, None, None, out, lse, ws)
+    o, l, to, tl = attention_and_bounds(R.f64(q[0]), R.decode(cache.K8), R.decode(cache.V8), R.f64(cache.k_scale),
+                                        R.f64(cache.v_scale))
+    assert np.all(np.abs(o).max(-1) > 50 * to.max(-1))  # no output of zeros, or of a few bits, is within the bounds
+    assert np.all(np.abs(R.f64(out[0]) - o) <= to), np.max(np.abs(R.f64(out[0]) - o) / to)
+    assert np.all(np.abs(R.f64(lse[0]) - l) <= tl), np.max(np.abs(R.f64(lse[0]) - l) / tl)
+
+
+# chunks, C, H, Hkv, sb, dtype: one part and cut runs, every grouping of heads
+SHAPES = [(6, 64, 4, 4, 64, "f32"), (30, 16, 8, 1, 16, "bf16"), (600, 32, 2, 1, 32, "bf16"), (600, 32, 16, 1, 8, "f32"),
+          (90, 64, 32, 8, 64, "bf16")]
+
+
+@pytest.mark.parametrize("n,C,H,Hkv,sb,dtype", SHAPES)
+@pytest.mark.parametrize("e", [20, 30, 40, 70, 100])
+@pytest.mark.parametrize("where", [0.0, 0.5, 1.0])
+def test_a_block_of_large_v_that_is_hardly_attended(lsa, n, C, H, Hkv, sb, dtype, e, where):
+    """A chunk whose V are 2^e times larger and whose weights are 2^-e e^-8 of the others': it adds little, and takes no
+    bits from the rest."""
+    at = int(where * (n - 1))
+    exps = np.full((n, Hkv, C // sb), -6.0)
+    exps[at] += e
+    check_scaled(lsa, *scaled_cache(lsa, n, C, H, Hkv, sb, dtype, exps, 50 + e, {at: -e * np.log(2) - 8}))
+
+
+@pytest.mark.parametrize("n,C,H,Hkv,sb,dtype", SHAPES)
+@pytest.mark.parametrize("kind", ["rising", "falling", "random", "least", "largest"])
+def test_v_scales_of_all_sizes(lsa, n, C, H, Hkv, sb, dtype, kind):
+    """Scales from 2^-120 to 2^110 over the sequence, in order and in none, and all of them at an end of the range."""
+    m = n * (C // sb)
+    e = {"rising": np.linspace(-120, 110, m), "falling": np.linspace(110, -120, m),
+         "random": np.random.default_rng(9).uniform(-120, 110, m), "least": np.full(m, -120.0),
+         "largest": np.full(m, 110.0)}[kind]
+    exps = np.round(e).reshape(n, 1, C // sb).repeat(Hkv, 1)
+    check_scaled(lsa, *scaled_cache(lsa, n, C, H, Hkv, sb, dtype, exps, 60))
+
+
+@pytest.mark.parametrize("n,C,H,Hkv,sb,dtype", SHAPES)
+def test_logits_that_rise_while_v_scales_fall(lsa, n, C, H, Hkv, sb, dtype):
+    """Each chunk's weights are up to 2^90 times the first's and its scales as many times smaller, so that all of them
+    count: the carried output is rescaled at every step, by weights and by scales in turn."""
+    bits = np.round(np.linspace(0, 90, n))
+    exps = (20 - bits)[:, None, None].repeat(Hkv, 1).repeat(C // sb, 2)
+    check_scaled(lsa, *scaled_cache(lsa, n, C, H, Hkv, sb, dtype, exps, 61,
+                                    {c: (bits[c] - 90) * np.log(2) for c in range(n)}))
