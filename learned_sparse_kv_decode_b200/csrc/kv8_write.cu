@@ -146,7 +146,8 @@ template <bool BF16>
 __device__ __forceinline__ void store_codes(uint8_t* row, int oa, int ob, OctetRaw<BF16> a, OctetRaw<BF16> b,
                                             float scale, bool power_of_two) {
     float x[8], y[8];
-    const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // 2^-e of a scale 2^e
+    // 2^-e of a scale 2^e; that of 2^127, which only an older block can have, is subnormal
+    const float inv = __uint_as_float(max((254u << 23) - __float_as_uint(scale), 1u << 22));
     if (BF16 && power_of_two) {
         const uint32_t w = __float_as_uint(inv), i2 = (w & 0xFFFF0000u) | w >> 16;
         auto mul = [i2](uint32_t& v) { asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(i2)); };

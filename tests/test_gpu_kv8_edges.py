@@ -1,11 +1,11 @@
 """GPU tests of the 8-bit K/V cache at values and sizes where a kernel's own number format, split or plan could show:
-non-finite queries, V scales of very unlike size."""
+non-finite queries, V scales of very unlike size, scales at the ends of the range under new rows."""
 import numpy as np
 import pytest
 import torch
 
 from tests import _kv8 as R
-from tests.test_gpu_kv8 import attn_inputs, i32, make_dims, tensor
+from tests.test_gpu_kv8 import attn_inputs, check_append, i32, make_dims, tensor
 
 pytestmark = pytest.mark.gpu
 DH = R.DH
@@ -167,3 +167,31 @@ def test_logits_that_rise_while_v_scales_fall(lsa, n, C, H, Hkv, sb, dtype):
     exps = (20 - bits)[:, None, None].repeat(Hkv, 1).repeat(C // sb, 2)
     check_scaled(lsa, *scaled_cache(lsa, n, C, H, Hkv, sb, dtype, exps, 61,
                                     {c: (bits[c] - 90) * np.log(2) for c in range(n)}))
+
+
+# ---------------------------------------------------------------- the write
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("e", [-126, -121, -120, 0, 119, 120, 121, 126, 127])
+def test_append_to_blocks_whose_scale_is_at_an_end_of_the_range(lsa, dtype, e):
+    """Rows of all sizes written behind older tokens, in blocks that came with a scale of 2^e: quotients by a power of two
+    are exact, so the codes are those of the definition."""
+    n_b, C, Hkv, sb, n, start = [2], 32, 2, 16, 20, 5
+    dims = make_dims(lsa, n_b, [1], C, 2, dtype)
+    r = np.random.default_rng(70)
+    t = R.make_cache(lsa, 2, Hkv, C, sb, r)
+    for name in ("k_scale", "v_scale"):
+        t[name].fill_(2.0 ** e)
+    size = np.exp2(np.where(np.arange(n) % 3 == 0, 126.0, r.uniform(-130, 126, n)))[None, :, None, None]
+    size[:, :11] *= 1.0 if e >= 0 else 2.0 ** -240  # below 0 the first block's scale stays as it is
+    x = np.clip(r.normal(0, 1, (1, n, 2 * Hkv, DH)) * size, -3.3e38, 3.3e38)
+    x[0, 3, :, :8] = 3.0 * 2.0 ** np.clip(np.arange(8) + e - 9.0, -149, 126)  # in and out of the codes' subnormals
+    rows = tensor(x.astype(np.float32), dtype)
+    before = {m: y.clone() for m, y in t.items()}
+    cache = lsa.Kv8Cache(dims, Hkv, sb, t["K8"], t["V8"], t["k_scale"], t["v_scale"])
+    ws = lsa.alloc_workspace(dims, kv8=cache)
+    lsa.lsa_kv8_append(dims, cache, None, rows[:, :, :Hkv], rows[:, :, Hkv:], i32([start]), None, ws)
+    check_append(before, t, R.f64(rows[:, :, :Hkv]), n_b, C, sb, [start], None, "K")
+    check_append(before, t, R.f64(rows[:, :, Hkv:]), n_b, C, sb, [start], None, "V")
+    assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
+    if e == 127:  # not all of them round to 0
+        assert bool((R.decode(t["K8"])[0, :, start:sb] != 0).any())
