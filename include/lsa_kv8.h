@@ -126,14 +126,18 @@ LSA_API lsa_status lsa_kv8_decode_attn(const lsa_dims *dims, const lsa_kv8_cache
                                        void *stream);
 
 /* A token's whole step over the 8-bit cache: write the new token's K/V (lsa_kv8_append, one row per
- * sequence at position seq_len[b]), prepare its queries, score the chunks, keep the top k, and attend
- * over the kept chunks' tokens below seq_len[b] + 1. seq_len itself is not changed: the caller adds one
- * after the step.
+ * sequence at position seq_len[b]), prepare its queries (also at position seq_len[b]), score the chunks, keep
+ * the top k, and attend over the kept chunks' tokens below seq_len[b] + 1. seq_len itself is not changed: the
+ * caller adds one after the step.
  *   prep           NULL: q and k are taken as they are
+ *   chunk_emb      the caller's, of every chunk that holds a token, the one being filled among them: a chunk is
+ *                  kept by its score alone, also the one that the new token was written to
  *   q, k, v        [B] rows of [H][Dh] (q) and [n_kv_heads][Dh] (k, v) kv_dtype, *_stride elements apart.
  *                  k and v both NULL: nothing is written, and the attention reads tokens below seq_len[b]
  *   seq_len        [B] int32 device, tokens cached before the step; may be NULL only if k and v are NULL
- *                  and prep is NULL
+ *                  and prep is NULL (every chunk is then full)
+ * Chunks that hold no token yet (behind seq_len[b] and the new token) are not compared: their embeddings may be
+ * anything, and they are named, lowest index first, only where fewer than k_b chunks hold tokens.
  * Other arguments as lsa_decode_step; without prep, q_stride must be H * Dh. */
 LSA_API lsa_status lsa_decode_step_kv8(const lsa_dims *dims, const lsa_kv8_cache *cache, const lsa_qk_prep *prep,
                                        const void *q_emb, const void *chunk_emb, const void *q, int64_t q_stride,

@@ -9,8 +9,9 @@ namespace lsa {
 cudaError_t launch_score(const lsa_dims& d, const SeqTable& tab, int max_n, const void* q_emb,
                          const void* chunk_emb, float* scores, uint32_t* err, int num_sms,
                          cudaStream_t stream, bool pdl);
-cudaError_t launch_topk(const lsa_dims& d, const SeqTable& tab, int max_n, const float* scores,
-                        int32_t* ids, uint32_t* err, cudaStream_t stream, bool pdl);
+cudaError_t launch_topk_live(const lsa_dims& d, const SeqTable& tab, int max_n, const float* scores,
+                             const int32_t* seq_len, int len_add, int32_t* ids, uint32_t* err, cudaStream_t stream,
+                             bool pdl);
 cudaError_t launch_qk_norm_rope(const lsa_dims& d, int n_kv_heads, const lsa_qk_prep& prep, int64_t n_tok,
                                 const int32_t* positions, const void* q, int64_t q_stride, const void* k,
                                 int64_t k_stride, void* q_out, int64_t qo_stride, void* k_out, int64_t ko_stride,
@@ -256,7 +257,9 @@ lsa_status lsa_decode_step_kv8(const lsa_dims* dims, const lsa_kv8_cache* cache,
     uint32_t* err = reinterpret_cast<uint32_t*>(ws);
     float* scores = reinterpret_cast<float*>(at(ws, c.w.base.scores));
     cudaError_t e = launch_score(*dims, c.p.tab, c.p.max_n, q_emb, chunk_emb, scores, err, c.di.sms, st, false);
-    if (e == cudaSuccess) e = launch_topk(*dims, c.p.tab, c.p.max_n, scores, chunk_ids_out, err, st, true);
+    const int len_add = k != nullptr ? 1 : 0;  // the new token counts
+    if (e == cudaSuccess)
+        e = launch_topk_live(*dims, c.p.tab, c.p.max_n, scores, seq_len, len_add, chunk_ids_out, err, st, true);
     // The write and the queries depend on neither: launched early, they run beside the top-k. Each waits
     // for the kernel before it at its end, so that the attention still follows all of them.
     if (e == cudaSuccess && k != nullptr)
@@ -271,7 +274,7 @@ lsa_status lsa_decode_step_kv8(const lsa_dims* dims, const lsa_kv8_cache* cache,
     }
     if (e == cudaSuccess)
         e = launch_kv8_attn(*dims, c.p.tab, *cache, c.g, c.di.sms, qr, chunk_ids_out, nullptr, seq_len,
-                            k != nullptr ? 1 : 0, reinterpret_cast<float*>(at(ws, c.w.part_o)),
+                            len_add, reinterpret_cast<float*>(at(ws, c.w.part_o)),
                             reinterpret_cast<float*>(at(ws, c.w.part_ml)), out, lse, err, st, true);
     return cuda_status(e);
 }

@@ -74,6 +74,19 @@ struct ThresholdArgs {
     int32_t* counts;
 };
 
+// Chunks at or behind a sequence's length hold no token yet: whatever their scores are (their embeddings may be
+// anything), they come after all others, lowest index first, and are not looked at for NaN. seq_len null: all count.
+struct LiveArgs {
+    const int32_t* seq_len;
+    int32_t len_add;  // added to seq_len
+};
+// Chunks of sequence b, of n, that hold tokens.
+__device__ __forceinline__ int live_chunks(const LiveArgs& lv, int b, int n, int C) {
+    if (lv.seq_len == nullptr) return n;
+    const int64_t c = ((int64_t)lv.seq_len[b] + lv.len_add + C - 1) / C;
+    return c < 0 ? 0 : c < n ? (int)c : n;
+}
+
 // Sum of one value per thread over the CTA and then the cluster (every thread gets the total).
 // `red` holds one slot per warp, `cta_total` one word that the cluster reads through DSMEM.
 template <int WARPS>
@@ -106,7 +119,7 @@ __device__ __forceinline__ uint32_t cluster_sum(uint32_t v, uint32_t* red, uint3
 template <bool SMEM_KEYS>
 __global__ void __launch_bounds__(kTopkThreads)
 k_topk(const float* __restrict__ scores, int32_t* __restrict__ ids, const SeqTable tab,
-       uint32_t* err, const ThresholdArgs th) {
+       uint32_t* err, const ThresholdArgs th, const LiveArgs lv) {
     extern __shared__ uint32_t skeys[];
     __shared__ uint32_t hist[2][256];  // double-buffered: pass p uses hist[p & 1]
     __shared__ uint32_t tot[256];
@@ -126,6 +139,7 @@ k_topk(const float* __restrict__ scores, int32_t* __restrict__ ids, const SeqTab
     const int slice = (n + (int)cs - 1) / (int)cs;
     const int lo = min(n, (int)rank * slice), hi = min(n, lo + slice);
     const int m = hi - lo;  // keys owned by this CTA: indices [lo, hi)
+    const int ml = max(0, min(m, live_chunks(lv, b, n, tab.C) - lo));  // of them with tokens: the first ml
     const float* s = scores + tab.chunk_off[b] + lo;
     int32_t* out = ids + tab.kept_off[b];
 
@@ -134,9 +148,9 @@ k_topk(const float* __restrict__ scores, int32_t* __restrict__ ids, const SeqTab
 
     bool bad = false;
     if constexpr (SMEM_KEYS) {
-        for (int i = tid; i < m; i += kTopkThreads) skeys[i] = score_key(s[i], bad);
+        for (int i = tid; i < m; i += kTopkThreads) skeys[i] = i < ml ? score_key(s[i], bad) : 0u;
     } else {
-        for (int i = tid; i < m; i += kTopkThreads) (void)score_key(s[i], bad);
+        for (int i = tid; i < ml; i += kTopkThreads) (void)score_key(s[i], bad);
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) set_error(err, kErrNonFinite);
 
@@ -145,7 +159,7 @@ k_topk(const float* __restrict__ scores, int32_t* __restrict__ ids, const SeqTab
             return skeys[i];
         } else {
             bool dummy = false;
-            return score_key(__ldg(s + i), dummy);
+            return i < ml ? score_key(__ldg(s + i), dummy) : 0u;
         }
     };
 
@@ -407,7 +421,7 @@ __device__ __forceinline__ int topk_stage_slot(int i) { return i + (i >> 5); }
 template <int R>
 __global__ void __launch_bounds__(kTopkRegThreads)
 k_topk_reg(const float* __restrict__ scores, int32_t* __restrict__ ids, const SeqTable tab,
-           uint32_t* err, const ThresholdArgs th) {
+           uint32_t* err, const ThresholdArgs th, const LiveArgs lv) {
     constexpr int kSlice = kTopkRegThreads * R;
     __shared__ uint32_t hist[3][256];
     __shared__ uint32_t tot[2][256];  // cluster totals: every CTA adds its histogram into each CTA's copy
@@ -425,6 +439,7 @@ k_topk_reg(const float* __restrict__ scores, int32_t* __restrict__ ids, const Se
     const int slice = (n + (int)cs - 1) / (int)cs;
     const int lo = min(n, (int)rank * slice), hi = min(n, lo + slice);
     const int m = hi - lo;                     // keys of this CTA: [lo, hi)
+    const int ml = max(0, min(m, live_chunks(lv, b, n, tab.C) - lo));  // of them with tokens: the first ml
     const int base = tid * R;                  // this thread's run: [base, base + R) within the slice
     const float* s = scores + tab.chunk_off[b] + lo;
     int32_t* out = ids + tab.kept_off[b];
@@ -445,12 +460,12 @@ k_topk_reg(const float* __restrict__ scores, int32_t* __restrict__ ids, const Se
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             const int i = j * kTopkRegThreads + tid;
-            v[j] = i < m ? s[i] : 0.f;
+            v[j] = i < ml ? s[i] : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             const int i = j * kTopkRegThreads + tid;
-            stage[topk_stage_slot(i)] = i < m ? score_key(v[j], bad) : 0u;
+            stage[topk_stage_slot(i)] = i < ml ? score_key(v[j], bad) : 0u;
         }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) set_error(err, kErrNonFinite);
@@ -588,7 +603,8 @@ int topk_cluster_size(int max_n) {
 }
 
 cudaError_t launch_topk_impl(const lsa_dims& d, const SeqTable& tab, int max_n, const float* scores,
-                             int32_t* ids, uint32_t* err, cudaStream_t stream, bool pdl, const ThresholdArgs& th) {
+                             int32_t* ids, uint32_t* err, cudaStream_t stream, bool pdl, const ThresholdArgs& th,
+                             const LiveArgs& lv) {
     const int cs = topk_cluster_size(max_n);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -607,33 +623,42 @@ cudaError_t launch_topk_impl(const lsa_dims& d, const SeqTable& tab, int max_n, 
     if (per_thread <= 16) {
         cfg.blockDim = dim3(kTopkRegThreads, 1, 1);
         cfg.dynamicSmemBytes = 0;
-        if (per_thread <= 1) return cudaLaunchKernelEx(&cfg, k_topk_reg<1>, scores, ids, tab, err, th);
-        if (per_thread <= 2) return cudaLaunchKernelEx(&cfg, k_topk_reg<2>, scores, ids, tab, err, th);
-        if (per_thread <= 4) return cudaLaunchKernelEx(&cfg, k_topk_reg<4>, scores, ids, tab, err, th);
-        if (per_thread <= 8) return cudaLaunchKernelEx(&cfg, k_topk_reg<8>, scores, ids, tab, err, th);
-        return cudaLaunchKernelEx(&cfg, k_topk_reg<16>, scores, ids, tab, err, th);
+        if (per_thread <= 1) return cudaLaunchKernelEx(&cfg, k_topk_reg<1>, scores, ids, tab, err, th, lv);
+        if (per_thread <= 2) return cudaLaunchKernelEx(&cfg, k_topk_reg<2>, scores, ids, tab, err, th, lv);
+        if (per_thread <= 4) return cudaLaunchKernelEx(&cfg, k_topk_reg<4>, scores, ids, tab, err, th, lv);
+        if (per_thread <= 8) return cudaLaunchKernelEx(&cfg, k_topk_reg<8>, scores, ids, tab, err, th, lv);
+        return cudaLaunchKernelEx(&cfg, k_topk_reg<16>, scores, ids, tab, err, th, lv);
     }
     cfg.blockDim = dim3(kTopkThreads, 1, 1);
     const size_t key_bytes = (size_t)slice * 4;
     if (key_bytes <= kTopkSmemKeyLimit) {
         cfg.dynamicSmemBytes = key_bytes;
-        return cudaLaunchKernelEx(&cfg, k_topk<true>, scores, ids, tab, err, th);
+        return cudaLaunchKernelEx(&cfg, k_topk<true>, scores, ids, tab, err, th, lv);
     }
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, k_topk<false>, scores, ids, tab, err, th);
+    return cudaLaunchKernelEx(&cfg, k_topk<false>, scores, ids, tab, err, th, lv);
 }
 
 cudaError_t launch_topk(const lsa_dims& d, const SeqTable& tab, int max_n, const float* scores,
                         int32_t* ids, uint32_t* err, cudaStream_t stream, bool pdl) {
     const ThresholdArgs none = {0, 0.f, 0, nullptr};
-    return launch_topk_impl(d, tab, max_n, scores, ids, err, stream, pdl, none);
+    return launch_topk_impl(d, tab, max_n, scores, ids, err, stream, pdl, none, LiveArgs{nullptr, 0});
+}
+
+// The kernels read seq_len before they wait for the kernel before them: that kernel does not write it, and whatever
+// did must have completed before that kernel began.
+cudaError_t launch_topk_live(const lsa_dims& d, const SeqTable& tab, int max_n, const float* scores,
+                             const int32_t* seq_len, int len_add, int32_t* ids, uint32_t* err, cudaStream_t stream,
+                             bool pdl) {
+    const ThresholdArgs none = {0, 0.f, 0, nullptr};
+    return launch_topk_impl(d, tab, max_n, scores, ids, err, stream, pdl, none, LiveArgs{seq_len, len_add});
 }
 
 cudaError_t launch_threshold(const lsa_dims& d, const SeqTable& tab, int max_n, const float* scores,
                              float tau, int k_min, int32_t* ids, int32_t* counts, uint32_t* err,
                              cudaStream_t stream, bool pdl) {
     const ThresholdArgs th = {1, tau, k_min, counts};
-    return launch_topk_impl(d, tab, max_n, scores, ids, err, stream, pdl, th);
+    return launch_topk_impl(d, tab, max_n, scores, ids, err, stream, pdl, th, LiveArgs{nullptr, 0});
 }
 
 }  // namespace lsa

@@ -1,5 +1,6 @@
 """GPU tests of the 8-bit K/V cache at values and sizes where a kernel's own number format, split or plan could show:
-non-finite queries, V scales of very unlike size, scales at the ends of the range under new rows."""
+non-finite queries, V scales of very unlike size, scales at the ends of the range under new rows, chunks
+that hold no token yet."""
 import numpy as np
 import pytest
 import torch
@@ -195,3 +196,49 @@ def test_append_to_blocks_whose_scale_is_at_an_end_of_the_range(lsa, dtype, e):
     assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
     if e == 127:  # not all of them round to 0
         assert bool((R.decode(t["K8"])[0, :, start:sb] != 0).any())
+
+
+# ---------------------------------------------------------------- the step's selection
+@pytest.mark.parametrize("N,k", [(12, 5), (12, 12), (300, 40), (1000, 7), (5000, 300), (33000, 64), (400000, 33)])
+def test_the_step_keeps_chunks_that_hold_tokens(lsa, N, k):
+    """Chunks behind a sequence's length have embeddings that would win, lose or be NaN, and are named only where too few
+    others are left. Sizes for every form of the selection."""
+    C, H, Hkv, E = 8, 2, 1, 4
+    lens = [N * C - 1, 0, 3 * C, 3 * C - 1, N * C // 2, (N - 1) * C]
+    B = len(lens) if N < 100000 else 2
+    lens = lens[:B] if N < 100000 else [N * C // 3, 5 * C + 1]
+    r = np.random.default_rng(N)
+    dims = make_dims(lsa, [N] * B, [k] * B, C, H, "f32", E=E)
+    cache = lsa.alloc_kv8_cache(dims, Hkv, 8)
+    cache.k_scale.fill_(2.0 ** -6)
+    cache.v_scale.fill_(2.0 ** -6)
+    for c in (cache.K8, cache.V8):
+        c.view(torch.uint8).random_(0, 126)
+    scores = -r.permutation(B * N).astype(np.float64) - 1
+    emb = np.zeros((B * N, E), dtype=np.float32)
+    emb[:, 0] = scores
+    empty = np.arange(N) >= -(-(np.asarray(lens)[:, None] + 1) // C)  # once the new token is there
+    fill = np.array([0.0, np.nan, np.inf, -np.inf, 1e30, -1e30], dtype=np.float32)
+    emb[empty.reshape(-1)] = fill[np.arange(empty.sum()) % 6][:, None]
+    emb[0, 1:] = 0.0
+    qe = np.zeros((B, 1, E), dtype=np.float32)
+    qe[:, :, 0] = 1.0
+    emb, qe = tensor(emb, "f32"), tensor(qe, "f32")
+    qkv = tensor(r.normal(0, 1, (B, H + 2 * Hkv, DH)), "f32")
+    q, kk, v = qkv[:, :H].contiguous(), qkv[:, H:H + Hkv], qkv[:, H + Hkv:]
+    ws = lsa.alloc_workspace(dims, kv8=cache)
+    ids = torch.full((B * k,), -7, dtype=torch.int32, device="cuda")
+    out, out2, lse, lse2 = (torch.empty(B, H, *x, device="cuda") for x in ((DH,), (DH,), (), ()))
+    for write in (True, False):
+        live = [-(-(n + write) // C) for n in lens]
+        lsa.lsa_decode_step_kv8(dims, cache, None, qe, emb, q, kk if write else None, v if write else None, i32(lens), ids,
+                                out, lse, ws)
+        got = ids.view(B, k).cpu().numpy()
+        for b, n in enumerate(live):
+            s = scores[b * N:b * N + n]
+            want = np.sort(np.argsort(-s, kind="stable")[:k])
+            want = np.concatenate([want, np.arange(n, n + max(0, k - n))])
+            assert np.array_equal(got[b], want), (b, n)
+        lsa.lsa_kv8_decode_attn(dims, cache, q, ids, None, i32([n + write for n in lens]), out2, lse2, ws)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+        assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
