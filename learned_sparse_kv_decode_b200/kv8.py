@@ -48,11 +48,27 @@ def _signatures():
 _signatures()
 
 
+def _view(address, n):
+    """The n bytes at an address, for comparisons."""
+    return (ctypes.c_char * n).from_address(address)
+
+
 class _Shape:
-    """What the checks need of a Dims: worked out once for each."""
+    """What the checks need of a Dims, with the bytes of the lsa_dims and its arrays that it was worked out from."""
 
     def __init__(self, dims):
-        c = dims.c
+        c = self.c = dims.c
+        if not 1 <= c.B <= abi.LSA_MAX_BATCH:
+            raise abi.LsaError(abi.LSA_ERR_INVALID_ARG, "Dims")
+        self.ptr = dims.ptr
+        views = [_view(ctypes.addressof(c), ctypes.sizeof(c))]
+        if c.chunk_offsets:
+            views.append(_view(ctypes.addressof(c.chunk_offsets.contents), 8 * (c.B + 1)))
+        if c.k_per_seq:
+            views.append(_view(ctypes.addressof(c.k_per_seq.contents), 4 * c.B))
+        views += views[:1] * (3 - len(views))
+        self.v0, self.v1, self.v2 = views
+        self.b0, self.b1, self.b2 = (v.raw for v in views)
         self.B, self.H, self.C = c.B, c.H, c.chunk_len
         self.dtype = torch.bfloat16 if c.kv_dtype == LSA_BF16 else torch.float32
         self.emb_dtype = torch.bfloat16 if c.emb_dtype == LSA_BF16 else torch.float32
@@ -61,10 +77,9 @@ class _Shape:
 
 
 def _shape(dims):
+    """The sizes that the C side will read from `dims`: worked out again when it was changed in place."""
     s = getattr(dims, "_kv8_shape", None)
-    if s is None:
-        if not 1 <= dims.c.B <= abi.LSA_MAX_BATCH:
-            raise abi.LsaError(abi.LSA_ERR_INVALID_ARG, "Dims")
+    if s is None or s.c is not dims.c or s.v0.raw != s.b0 or s.v1.raw != s.b1 or s.v2.raw != s.b2:
         s = dims._kv8_shape = _Shape(dims)
     return s
 
@@ -246,7 +261,7 @@ def lsa_qk_norm_rope(dims, prep, positions, q, k, q_out, k_out, stream=None) -> 
         hkv = k.shape[-2] if k.dim() > 1 else 0
         kp, ks = _rows(k, "k", s.dtype, n, hkv, d)
         ko, kos = _rows(k_out, "k_out", s.dtype, n, hkv, d)
-    _check(lib.lsa_qk_norm_rope(dims.ptr, hkv or 1, prep.check(d), n, _ptr(positions, "positions", torch.int32, n, d),
+    _check(lib.lsa_qk_norm_rope(s.ptr, hkv or 1, prep.check(d), n, _ptr(positions, "positions", torch.int32, n, d),
                                 qp, qs or 0, kp, ks or 0, qo, qos or 0, ko, kos or 0, _stream(stream, d)),
            "lsa_qk_norm_rope")
 
@@ -260,7 +275,7 @@ def lsa_kv8_append(dims, cache, prep, k, v, start, new_count, ws, stream=None) -
     kp, ks = _rows(k, "k", s.dtype, s.B * n, cache.n_kv_heads, d)
     vp, vs = _rows(v, "v", s.dtype, s.B * n, cache.n_kv_heads, d)
     wp, wn = _ws(ws, d)
-    _check(lib.lsa_kv8_append(dims.ptr, cache.ptr, None if prep is None else prep.check(d), n, kp, ks, vp, vs,
+    _check(lib.lsa_kv8_append(s.ptr, cache.ptr, None if prep is None else prep.check(d), n, kp, ks, vp, vs,
                               _opt(start, "start", torch.int32, s.B, d),
                               _opt(new_count, "new_count", torch.int32, s.B, d), wp, wn, _stream(stream, d)),
            "lsa_kv8_append")
@@ -271,7 +286,7 @@ def lsa_kv8_gather(dims, cache, chunk_ids, seq_len, K_res, V_res, ws, stream=Non
     d = cache.check(s)
     n = (s.chunks if chunk_ids is None else s.kept) * s.C * cache.n_kv_heads * LSA_HEAD_DIM
     wp, wn = _ws(ws, d)
-    _check(lib.lsa_kv8_gather(dims.ptr, cache.ptr, _opt(chunk_ids, "chunk_ids", torch.int32, s.kept, d),
+    _check(lib.lsa_kv8_gather(s.ptr, cache.ptr, _opt(chunk_ids, "chunk_ids", torch.int32, s.kept, d),
                               _opt(seq_len, "seq_len", torch.int32, s.B, d), _ptr(K_res, "K_res", s.dtype, n, d),
                               _ptr(V_res, "V_res", s.dtype, n, d), wp, wn, _stream(stream, d)), "lsa_kv8_gather")
 
@@ -281,7 +296,7 @@ def lsa_kv8_decode_attn(dims, cache, q, chunk_ids, kept_count, seq_len, out, lse
     d = cache.check(s)
     n = s.B * s.H
     wp, wn = _ws(ws, d)
-    _check(lib.lsa_kv8_decode_attn(dims.ptr, cache.ptr, _ptr(q, "q", s.dtype, n * LSA_HEAD_DIM, d),
+    _check(lib.lsa_kv8_decode_attn(s.ptr, cache.ptr, _ptr(q, "q", s.dtype, n * LSA_HEAD_DIM, d),
                                    _opt(chunk_ids, "chunk_ids", torch.int32, s.kept, d),
                                    _opt(kept_count, "kept_count", torch.int32, s.B, d),
                                    _opt(seq_len, "seq_len", torch.int32, s.B, d),
@@ -304,7 +319,7 @@ def lsa_decode_step_kv8(dims, cache, prep, q_emb, chunk_emb, q, k, v, seq_len, c
         vp, vs = _rows(v, "v", s.dtype, s.B, cache.n_kv_heads, d)
     wp, wn = _ws(ws, d)
     c = dims.c
-    _check(lib.lsa_decode_step_kv8(dims.ptr, cache.ptr, None if prep is None else prep.check(d),
+    _check(lib.lsa_decode_step_kv8(s.ptr, cache.ptr, None if prep is None else prep.check(d),
                                    _ptr(q_emb, "q_emb", s.emb_dtype, s.B * c.Q * c.E, d),
                                    _ptr(chunk_emb, "chunk_emb", s.emb_dtype, s.chunks * c.E, d), qp, qs, kp, ks or 0,
                                    vp, vs or 0, _opt(seq_len, "seq_len", torch.int32, s.B, d),
