@@ -96,6 +96,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A partial's maximum as it is stored. The merge takes -inf for a partial without tokens; scores that are all NaN leave
+// the maximum so too (fmaxf passes NaN over), with a sum of NaN, which any finite maximum carries on to the output.
+__device__ __forceinline__ float part_max(float m, float l) { return m == -INFINITY && l != 0.f ? 0.f : m; }
+
 __device__ __forceinline__ void consumer_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(kAttnConsumers) : "memory");
 }
@@ -281,7 +285,7 @@ k_attn_split(const uint8_t* __restrict__ q, const uint8_t* __restrict__ K,
                 for (int e = 0; e < VEC; e += 4)
                     *reinterpret_cast<float4*>(po + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
                 if (li == 0) {
-                    pml[0] = m;
+                    pml[0] = part_max(m, l);
                     pml[1] = l;
                 }
             }
@@ -313,7 +317,7 @@ k_attn_split(const uint8_t* __restrict__ q, const uint8_t* __restrict__ K,
                 for (int e = 0; e < VEC; e += 4)
                     *reinterpret_cast<float4*>(po + e) = make_float4(A[e], A[e + 1], A[e + 2], A[e + 3]);
                 if (li == 0) {
-                    pml[0] = M;
+                    pml[0] = part_max(M, L);
                     pml[1] = L;
                 }
             }

@@ -1,0 +1,65 @@
+"""GPU tests that queries and keys which are not finite give NaN, in every attention over the 16- and 32-bit caches: a
+softmax over such logits is NaN, and an output of zeros would say that there was nothing to attend to."""
+import numpy as np
+import pytest
+import torch
+
+import datagen
+from tests import _gpu as G
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lsa():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import learned_sparse_kv_decode_b200 as m
+    return m
+
+
+def kept(w, seed):
+    r = np.random.default_rng(seed)
+    return torch.from_numpy(np.concatenate(
+        [np.sort(r.permutation(n)[:k]) for n, k in zip(w.N, w.k)]).astype(np.int32)).cuda()
+
+
+def check(call, q, out, lse, out0, lse0, b, h, value):
+    """`call(q)` with `value` in one row of q: that row's output is NaN, the others keep their bits."""
+    bad = q.clone()
+    bad[b, h, 77] = value
+    out.fill_(7.0)
+    lse.fill_(7.0)
+    call(bad)
+    assert bool(torch.isnan(out[b, h]).all()) and bool(torch.isnan(lse[b, h]).all())
+    rest = torch.ones(lse.shape, dtype=torch.bool, device="cuda")
+    rest[b, h] = False
+    assert torch.equal(out[rest], out0[rest]) and torch.equal(lse[rest], lse0[rest])
+
+
+VALUES = [float("nan"), float("inf"), float("-inf")]
+
+
+@pytest.mark.parametrize("kv_dtype,H", [("bf16", 16), ("bf16", 128), ("f32", 8), ("bf16", 1)])
+def test_sparse_attention(lsa, kv_dtype, H):
+    w = datagen.small_workload(B=3, N=(40, 9, 200), k=(11, 9, 200), C=64, E=64, H=H, kv_dtype=kv_dtype, seed=71)
+    dw = G.DeviceWorkload(w, lsa)
+    ids = kept(w, 1)
+    counts = torch.tensor([7, 0, 200], dtype=torch.int32, device="cuda")
+    calls = {
+        "ids": lambda q: lsa.lsa_sparse_decode_attn(dw.dims, q, dw.K, dw.V, ids, dw.out, dw.lse, dw.ws),
+        "counts": lambda q: lsa.lsa_sparse_decode_attn_counts(dw.dims, q, dw.K, dw.V, ids, counts, dw.out, dw.lse, dw.ws),
+        "noalloc": lambda q: lsa.lsa_sparse_decode_attn_noalloc(dw.dims, q, dw.K, dw.V, ids, dw.out, dw.lse),
+    }
+    if H == 128:  # more partials than the library's fixed scratch holds
+        with pytest.raises(lsa.LsaError):
+            calls.pop("noalloc")(dw.q)
+    for name, call in calls.items():
+        call(dw.q)
+        out0, lse0 = dw.out.clone(), dw.lse.clone()
+        for b, h, value in zip((0, 2, 2), (0, H - 1, H // 2), VALUES):
+            check(call, dw.q, dw.out, dw.lse, out0, lse0, b, h, value)
+        if name == "counts":
+            assert bool((dw.out[1] == 0).all()) and bool((dw.lse[1] == -np.inf).all())
+    dw.K[int(w.chunk_offsets[1]) * w.C:int(w.chunk_offsets[2]) * w.C, 0] = float("nan")  # all keys of one sequence
+    calls["ids"](dw.q)
+    assert bool(torch.isnan(dw.out[1, 0]).all()) and bool(torch.isfinite(dw.out[[0, 2]]).all())
