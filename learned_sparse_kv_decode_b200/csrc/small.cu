@@ -75,6 +75,13 @@ __device__ __forceinline__ float small_ex2(float x) {
     return y;
 }
 
+// Maximum that passes a NaN on: a NaN score makes its row NaN, and is not taken for a token past the chunk.
+__device__ __forceinline__ float small_max(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // grid (max k_b, H, B), kSmallThreads threads; with CL, clusters of (max k_b, 1, 1).
 // EBF16: embeddings are bf16 (else fp32); KBF16: q, K, V are bf16 (else fp32).
 template <bool EBF16, bool KBF16, bool CL>
@@ -208,7 +215,7 @@ k_decode_small(const uint8_t* __restrict__ q_emb, const uint8_t* __restrict__ em
             }
             float mx = m;
 #pragma unroll
-            for (int u = 0; u < kSmallUnroll; ++u) mx = fmaxf(mx, s[u]);
+            for (int u = 0; u < kSmallUnroll; ++u) mx = small_max(mx, s[u]);
             if (mx == -INFINITY) continue;  // every token of this step is past the chunk (uniform per group)
             const float corr = m == -INFINITY ? 0.f : small_ex2(m - mx);
             l *= corr;
@@ -275,7 +282,7 @@ k_decode_small(const uint8_t* __restrict__ q_emb, const uint8_t* __restrict__ em
                 A = fmaf(w, small_dsmem_ld(&s_fin[tid], (uint32_t)c), A);
                 L = fmaf(w, small_dsmem_ld(&s_fin[kDh + 1], (uint32_t)c), L);
             }
-            out[((int64_t)b * H + h) * kDh + tid] = L > 0.f ? A / L : 0.f;
+            out[((int64_t)b * H + h) * kDh + tid] = L == 0.f ? 0.f : A / L;
             if (lse != nullptr && tid == 0) lse[(int64_t)b * H + h] = (M + log2f(L)) * 0.69314718055994531f;
         }
         small_cluster_sync();  // every CTA's shared memory stays alive until CTA 0 has read it
@@ -304,7 +311,7 @@ k_decode_small(const uint8_t* __restrict__ q_emb, const uint8_t* __restrict__ em
             A = fmaf(w, __ldcg(pc + tid), A);
             L = fmaf(w, __ldcg(pc + kDh + 1), L);
         }
-        out[((int64_t)b * H + h) * kDh + tid] = L > 0.f ? A / L : 0.f;
+        out[((int64_t)b * H + h) * kDh + tid] = L == 0.f ? 0.f : A / L;
         if (lse != nullptr && tid == 0) lse[(int64_t)b * H + h] = (M + log2f(L)) * 0.69314718055994531f;
         if (tid == 0) *counter = 0u;  // every CTA of (b, h) has arrived: ready for the next call
     }

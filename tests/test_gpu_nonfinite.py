@@ -63,3 +63,24 @@ def test_sparse_attention(lsa, kv_dtype, H):
     dw.K[int(w.chunk_offsets[1]) * w.C:int(w.chunk_offsets[2]) * w.C, 0] = float("nan")  # all keys of one sequence
     calls["ids"](dw.q)
     assert bool(torch.isnan(dw.out[1, 0]).all()) and bool(torch.isfinite(dw.out[[0, 2]]).all())
+
+
+@pytest.mark.parametrize("B,N,k,C,H,kv_dtype", [(1, 64, 8, 64, 8, "f32"), (2, 20, 3, 8, 4, "bf16"), (1, 40, 1, 16, 2, "f32"),
+                                                (2, 50, 20, 32, 4, "bf16")])
+def test_one_launch_step(lsa, B, N, k, C, H, kv_dtype):
+    w = datagen.small_workload(B=B, N=(N,) * B, k=(k,) * B, C=C, E=64, H=H, kv_dtype=kv_dtype, seed=72)
+    dw = G.DeviceWorkload(w, lsa)
+
+    def call(q):
+        lsa.lsa_decode_step(dw.dims, dw.q_emb, dw.chunk_emb, q, dw.K, dw.V, dw.ids, dw.out, dw.lse, dw.ws)
+
+    call(dw.q)
+    out0, lse0 = dw.out.clone(), dw.lse.clone()
+    for h, value in zip((0, H - 1, H // 2), VALUES):
+        check(call, dw.q, dw.out, dw.lse, out0, lse0, B - 1, h, value)
+    first = int(dw.ids[0])
+    dw.K[first * C + 3, 0, 5] = float("nan")  # one key of one head
+    call(dw.q)
+    assert bool(torch.isnan(dw.out[0, 0]).all()) and bool(torch.isnan(dw.lse[0, 0]))
+    assert torch.equal(dw.out[0, 1:], out0[0, 1:])
+    assert lsa.lsa_get_device_status(dw.ws) == lsa.LSA_OK
