@@ -766,9 +766,10 @@ k_attn_la(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                                         : part_o + (slot * lp.Qw + r0) * kDh;
                     float* dst1 = whole ? out + (((int64_t)cur.b * lp.Qw + r1) * lp.H + cur.h) * kDh
                                         : part_o + (slot * lp.Qw + r1) * kDh;
-                    // no valid token at all (every id bad): out 0, lse -inf
-                    const float inv0 = whole ? (LL0 > 0.f ? 1.f / LL0 : 0.f) : 1.f;
-                    const float inv1 = whole ? (LL1 > 0.f ? 1.f / LL1 : 0.f) : 1.f;
+                    // no valid token at all (every id bad): out 0, lse -inf. Scores that are all NaN leave
+                    // the maximum at -inf too (fmaxf passes NaN over), but the sum is NaN
+                    const float inv0 = whole ? (LL0 == 0.f ? 0.f : 1.f / LL0) : 1.f;
+                    const float inv1 = whole ? (LL1 == 0.f ? 0.f : 1.f / LL1) : 1.f;
 #pragma unroll 1
                     for (int w = 0; w < 2; ++w) {
                         uint32_t oa[32], ob[32];
@@ -802,8 +803,11 @@ k_attn_la(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                                 if (wr1) lse[((int64_t)cur.b * lp.Qw + r1) * lp.H + cur.h] = (M1 + log2f(LL1)) * kLn2;
                             }
                         } else {
-                            if (wr0) *reinterpret_cast<float2*>(part_ml + (slot * lp.Qw + r0) * 2) = make_float2(M0, LL0);
-                            if (wr1) *reinterpret_cast<float2*>(part_ml + (slot * lp.Qw + r1) * 2) = make_float2(M1, LL1);
+                            // the merge takes a maximum of -inf for a part without valid tokens
+                            const float s0 = M0 == -INFINITY && LL0 != 0.f ? 0.f : M0;
+                            const float s1 = M1 == -INFINITY && LL1 != 0.f ? 0.f : M1;
+                            if (wr0) *reinterpret_cast<float2*>(part_ml + (slot * lp.Qw + r0) * 2) = make_float2(s0, LL0);
+                            if (wr1) *reinterpret_cast<float2*>(part_ml + (slot * lp.Qw + r1) * 2) = make_float2(s1, LL1);
                         }
                     }
                 }
@@ -880,7 +884,7 @@ k_attn_la_merge(const float* __restrict__ part_o, const float* __restrict__ part
         }
         M = Mn;
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;  // no valid token (every id bad): out 0, lse -inf
+    const float inv = L == 0.f ? 0.f : 1.f / L;  // no valid token (every id bad): out 0, lse -inf
     float* dst = out + (((int64_t)b * lp.Qw + q) * lp.H + h) * kDh + lane * 4;
     *reinterpret_cast<float4*>(dst) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (lse != nullptr && lane == 0) lse[((int64_t)b * lp.Qw + q) * lp.H + h] = (M + log2f(L)) * la::kLn2;

@@ -84,3 +84,27 @@ def test_one_launch_step(lsa, B, N, k, C, H, kv_dtype):
     assert bool(torch.isnan(dw.out[0, 0]).all()) and bool(torch.isnan(dw.lse[0, 0]))
     assert torch.equal(dw.out[0, 1:], out0[0, 1:])
     assert lsa.lsa_get_device_status(dw.ws) == lsa.LSA_OK
+
+
+@pytest.mark.parametrize("B,N,k,C,Q,H", [(2, (40, 72), (5, 9), 64, 64, 4), (1, (9,), (1,), 64, 64, 1),
+                                         (1, (600,), (600,), 64, 7, 1), (3, (30, 50, 8), (7, 3, 8), 16, 33, 2)])
+def test_lookahead_attention(lsa, B, N, k, C, Q, H):
+    w = datagen.small_workload(B=B, N=N, k=k, C=C, Q=Q, E=64, H=H, kv_dtype="bf16", seed=73)
+    dw = G.DeviceWorkload(w, lsa)
+    q = G.to_device(datagen.make_lookahead_queries(w), "bf16").view(B, Q * H, w.Dh)
+    out, lse = torch.empty(B, Q * H, w.Dh, device="cuda"), torch.empty(B, Q * H, device="cuda")
+    ids = kept(w, 2)
+
+    def call(x):
+        lsa.lsa_sparse_decode_attn_lookahead(dw.dims, x, dw.K, dw.V, ids, out, lse, dw.ws)
+
+    call(q)
+    out0, lse0 = out.clone(), lse.clone()
+    assert bool(torch.isfinite(out0).all())
+    for row, value in zip((0, Q * H - 1, Q * H // 2), VALUES):
+        check(call, q, out, lse, out0, lse0, B - 1, row, value)
+    dw.K[int(w.chunk_offsets[B - 1]) * C + int(ids[-1]) * C + 2, 0, 5] = float("nan")
+    call(q)
+    nan = torch.isnan(out.view(B, Q, H, w.Dh))
+    assert bool(nan[B - 1, :, 0].all()) and not bool(nan[:, :, 1:].any()) and not bool(nan[:B - 1].any())
+    assert lsa.lsa_get_device_status(dw.ws) == lsa.LSA_OK
