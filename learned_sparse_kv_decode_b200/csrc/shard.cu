@@ -119,17 +119,15 @@ k_merge_partials(const float* __restrict__ outs, const float* __restrict__ lses,
     float M = -INFINITY;
     for (int g = 0; g < G; ++g) M = fmaxf(M, lses[((size_t)g * B + b) * H + h]);
     float L = 0.f, A = 0.f;
-    if (M != -INFINITY) {
-        for (int g = 0; g < G; ++g) {
-            const float lg = lses[((size_t)g * B + b) * H + h];
-            if (lg == -INFINITY) continue;  // a rank that kept nothing
-            const float wgt = expf(lg - M);
-            L += wgt;
-            A = fmaf(wgt, outs[(((size_t)g * B + b) * H + h) * kDh + d], A);
-        }
+    for (int g = 0; g < G; ++g) {
+        const float lg = lses[((size_t)g * B + b) * H + h];
+        if (lg == -INFINITY) continue;  // a rank that kept nothing (a NaN, which the maximum passes over, is not one)
+        const float wgt = expf(lg - M);
+        L += wgt;
+        A = fmaf(wgt, outs[(((size_t)g * B + b) * H + h) * kDh + d], A);
     }
-    out[((size_t)b * H + h) * kDh + d] = L > 0.f ? A / L : 0.f;
-    if (lse != nullptr && d == 0) lse[(size_t)b * H + h] = L > 0.f ? M + logf(L) : -INFINITY;
+    out[((size_t)b * H + h) * kDh + d] = L == 0.f ? 0.f : A / L;
+    if (lse != nullptr && d == 0) lse[(size_t)b * H + h] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
 cudaError_t launch_shard_candidates(const SeqTable& tab, int B, const ShardOffsets& offs, int k_pad,

@@ -108,3 +108,31 @@ def test_lookahead_attention(lsa, B, N, k, C, Q, H):
     nan = torch.isnan(out.view(B, Q, H, w.Dh))
     assert bool(nan[B - 1, :, 0].all()) and not bool(nan[:, :, 1:].any()) and not bool(nan[:B - 1].any())
     assert lsa.lsa_get_device_status(dw.ws) == lsa.LSA_OK
+
+
+def test_merge_of_partials(lsa):
+    """A rank's NaN reaches the merged output; a rank that kept nothing (lse = -inf) does not take part, whatever it holds."""
+    G_, B, H, Dh = 3, 2, 4, 128
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    outs = torch.randn(G_, B, H, Dh, generator=gen, device="cuda")
+    lses = torch.randn(G_, B, H, generator=gen, device="cuda")
+    lses[1, 0, 1], outs[1, 0, 1] = -np.inf, 0.0
+    lses[:, 1, 2], outs[:, 1, 2] = -np.inf, 0.0
+    out, lse = torch.empty(B, H, Dh, device="cuda"), torch.empty(B, H, device="cuda")
+    lsa.lsa_merge_partials(G_, B, H, outs, lses, out, lse)
+    out0, lse0 = out.clone(), lse.clone()
+    assert bool(torch.isfinite(out0).all()) and bool((out0[1, 2] == 0).all()) and float(lse0[1, 2]) == -np.inf
+    p = torch.softmax(lses.double(), 0)
+    want = (p[..., None] * outs.double()).sum(0)
+    ok = torch.ones(B, H, dtype=torch.bool, device="cuda")
+    ok[1, 2] = False
+    torch.testing.assert_close(out0[ok].double(), want[ok], rtol=0, atol=1e-5)
+    nan = float("nan")
+    lses[2, 0, 0], outs[2, 0, 0] = nan, nan                 # one rank of three
+    lses[:, 0, 3], outs[:, 0, 3] = nan, nan                 # every rank
+    lses[0, 1, 2], outs[0, 1, 2] = nan, nan                 # the others kept nothing
+    lsa.lsa_merge_partials(G_, B, H, outs, lses, out, lse)
+    hit = torch.zeros(B, H, dtype=torch.bool, device="cuda")
+    hit[0, 0] = hit[0, 3] = hit[1, 2] = True
+    assert bool(torch.isnan(out[hit]).all()) and bool(torch.isnan(lse[hit]).all())
+    assert torch.equal(out[~hit], out0[~hit]) and torch.equal(lse[~hit], lse0[~hit])
