@@ -1,12 +1,12 @@
 """GPU tests of the 8-bit K/V cache at values and sizes where a kernel's own number format, split or plan could show:
 non-finite queries, V scales of very unlike size, scales at the ends of the range under new rows, chunks
-that hold no token yet."""
+that hold no token yet, one key that takes all the weight, many K/V heads."""
 import numpy as np
 import pytest
 import torch
 
 from tests import _kv8 as R
-from tests.test_gpu_kv8 import attn_inputs, check_append, i32, make_dims, tensor
+from tests.test_gpu_kv8 import append_case, attn_inputs, check_append, i32, kept_ids, make_dims, prep_inputs, tensor
 
 pytestmark = pytest.mark.gpu
 DH = R.DH
@@ -119,7 +119,7 @@ def scaled_cache(lsa, n, C, H, Hkv, sb, dtype, exponents, seed, low=()):
     return dims, cache, q
 
 
-def check_scaled(lsa, dims, cache, q, ids=None, chunks=None):
+def check_scaled(lsa, dims, cache, q):
     H = q.shape[1]
     out, lse = torch.empty(1, H, DH, device="cuda"), torch.empty(1, H, device="cuda")
     ws = lsa.alloc_workspace(dims, kv8=cache)
@@ -242,3 +242,133 @@ def test_the_step_keeps_chunks_that_hold_tokens(lsa, N, k):
         lsa.lsa_kv8_decode_attn(dims, cache, q, ids, None, i32([n + write for n in lens]), out2, lse2, ws)
         assert torch.equal(out, out2) and torch.equal(lse, lse2)
         assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
+
+
+# ---------------------------------------------------------------- sharp softmax
+@pytest.mark.parametrize("n,C,H,Hkv,sb,dtype", SHAPES)
+@pytest.mark.parametrize("at", [0, 17, -1])
+def test_one_key_that_takes_all_the_weight(lsa, n, C, H, Hkv, sb, dtype, at):
+    """Queries of sizes 1 to 10000 and a key whose logit is 40 and more above all others: the output is that token's V. Its
+    own weight cancels in the quotient, so what is left is the halves and sums (2^-18 and 2^-23 a step, relative), the
+    low halves' end, 2^-38 of its scale times the largest code for each token, and what the other tokens weigh."""
+    r = np.random.default_rng(80 + n)
+    at = at % (n * C)
+    exps = r.integers(-10, -2, (n, Hkv, C // sb)).astype(np.float64)
+    dims, cache, q = scaled_cache(lsa, n, C, H, Hkv, sb, dtype, exps, 81)
+    q = (q.double() * torch.logspace(0, 4, H, dtype=torch.float64, device="cuda")[:, None]).to(q.dtype)
+    base = R.f64(q[0, 0])
+    key = torch.from_numpy(2.0 * base / 2.0 ** -5).float().cuda().to(torch.float8_e4m3fn)  # its block's scale becomes 2^-5
+    cache.k_scale[at // C, :, at % C // sb] = 2.0 ** -5
+    cache.K8[at // C, :, at % C] = key
+    K, V, ks, vs = R.decode(cache.K8), R.decode(cache.V8), R.f64(cache.k_scale), R.f64(cache.v_scale)
+    out, lse = torch.empty(1, H, DH, device="cuda"), torch.empty(1, H, device="cuda")
+    lsa.lsa_kv8_decode_attn(dims, cache, q, None, None, None, out, lse, lsa.alloc_workspace(dims, kv8=cache))
+    for h in range(H):
+        kv, x = h // (H // Hkv), R.f64(q[0, h])
+        k = K[:, kv].reshape(-1, DH) * np.repeat(ks[:, kv], sb, -1).reshape(-1, 1)
+        logit = k @ x / np.sqrt(DH)
+        A = np.abs(k) @ np.abs(x) / np.sqrt(DH)
+        assert logit.argmax() == at
+        gap = (logit[at] - logit - 2.0 ** -18 * (A + A[at]))[np.arange(len(logit)) != at].min()
+        assert gap > 30.0  # 40 and more, but for what the logits may be off
+        s = vs[at // C, kv, at % C // sb]
+        v = V[at // C, kv, at % C] * s
+        steps = (len(logit) / 16 + 64) * 2.0 ** -23
+        rest = len(logit) * np.exp(-gap) * 448 * vs.max()
+        tol = np.abs(v) * (2.0 ** -18 + 2 * steps) + len(logit) * 448 * 2.0 ** -38 * s + 2 * rest
+        assert np.all(np.abs(R.f64(out[0, h]) - v) <= tol), (h, np.max(np.abs(R.f64(out[0, h]) - v) / tol))
+        tol = 2.0 ** -18 * A[at] + 2.0 ** -18 + steps + 2 * len(logit) * np.exp(-gap) + 2.0 ** -22 * abs(logit[at])
+        assert abs(float(lse[0, h]) - logit[at]) <= tol
+
+
+# ---------------------------------------------------------------- many K/V heads
+@pytest.mark.parametrize("Hkv", [32, 64, 128])
+@pytest.mark.parametrize("dtype,B,n", [("bf16", 1, 1), ("f32", 2, 1), ("bf16", 3, 70), ("f32", 2, 130), ("bf16", 6, 300)])
+def test_append_of_many_heads(lsa, dtype, B, n, Hkv):
+    """Rows as they are against the definition, prepared ones against the two separate calls."""
+    C, sb = 64, 32
+    n_b = [n // C + 2 + b % 2 for b in range(B)]
+    starts, counts = [(29 * b + 5) % 65 for b in range(B)], [max(1, n - 13 * b) for b in range(B)]
+    dims, t, k, v = append_case(lsa, n_b, C, Hkv, sb, dtype, n, 90 + B, 1.5)
+    got = [{m: x.clone() for m, x in t.items()} for _ in range(3)]
+    ca, cb, cc = (lsa.Kv8Cache(dims, Hkv, sb, y["K8"], y["V8"], y["k_scale"], y["v_scale"]) for y in got)
+    ws = lsa.alloc_workspace(dims, kv8=ca)
+    lsa.lsa_kv8_append(dims, ca, None, k, v, i32(starts), i32(counts), ws)
+    check_append(t, got[0], R.f64(k), n_b, C, sb, starts, counts, "K")
+    check_append(t, got[0], R.f64(v), n_b, C, sb, starts, counts, "V")
+    _, _, inv, w = prep_inputs(1, 1, 1, dtype, 128, True, 2, 14)
+    for inter in (False, True):
+        prep = lsa.QkPrep(128, inv, None, w[1], 1e-5, inter)
+        for c in got[1:]:
+            for m in t:
+                c[m].copy_(t[m])
+        lsa.lsa_kv8_append(dims, cb, prep, k, v, i32(starts), i32(counts), ws)
+        pos = (torch.tensor(starts)[:, None] + torch.arange(n)).to(torch.int32).cuda()
+        kp = torch.empty((B, n, Hkv, DH), dtype=k.dtype, device="cuda")
+        lsa.lsa_qk_norm_rope(dims, prep, pos.view(-1), None, k.contiguous().view(-1, Hkv, DH), None, kp.view(-1, Hkv, DH))
+        lsa.lsa_kv8_append(dims, cc, None, kp, v, i32(starts), i32(counts), ws)
+        for m in t:
+            assert torch.equal(got[1][m].view(torch.uint8), got[2][m].view(torch.uint8)), m
+    assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
+
+
+@pytest.mark.parametrize("H,Hkv", [(32, 32), (64, 32), (64, 64), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_and_read_back_of_many_heads(lsa, H, Hkv, dtype):
+    n_b, k_b, C, sb = [30, 4], [21, 4], 32, 16
+    lens = [30 * 32 - 9, 70]
+    dims, cache, q = attn_inputs(lsa, n_b, C, H, Hkv, sb, dtype, lens, "append", 91, k_b)
+    q *= 0.02  # codes of up to 448 times 2^-6: keeps the logits within tens
+    ids = kept_ids(n_b, k_b, 3)
+    ws = lsa.alloc_workspace(dims, kv8=cache)
+    out, lse = torch.empty(2, H, DH, device="cuda"), torch.empty(2, H, device="cuda")
+    lsa.lsa_kv8_decode_attn(dims, cache, q, i32(np.concatenate(ids)), None, i32(lens), out, lse, ws)
+    K, V = (torch.full((sum(k_b) * C, Hkv, DH), 7.0, dtype=q.dtype, device="cuda") for _ in range(2))
+    lsa.lsa_kv8_gather(dims, cache, i32(np.concatenate(ids)), i32(lens), K, V, ws)
+    at, off = 0, 0
+    for b, kept in enumerate(ids):
+        pos = (kept[:, None] * C + np.arange(C)).reshape(-1)
+        ok = pos < lens[b]
+        chunk, within = off + pos[ok] // C, pos[ok] % C
+        rows = [R.decode(c)[chunk, :, within] * R.f64(sc)[chunk, :, within // sb][..., None]
+                for c, sc in ((cache.K8, cache.k_scale), (cache.V8, cache.v_scale))]
+        for got, want in zip((K, V), rows):
+            mine = got[at:at + len(pos)]
+            assert torch.equal(mine[torch.from_numpy(ok)].cpu(), torch.from_numpy(want).to(q.dtype))
+            assert bool((mine[torch.from_numpy(~ok)] == 7.0).all())
+        k, v = (x.transpose(1, 0, 2)[:, None] for x in rows)  # [Hkv][1][n][128]: one chunk of all the tokens
+        one = np.ones((1, Hkv, 1))
+        vs = R.f64(cache.v_scale)[chunk, :, within // sb]     # and the codes' scales, for the bound
+        o, l, to, tl = attention_and_bounds(R.f64(q[b]), k.transpose(1, 0, 2, 3), v.transpose(1, 0, 2, 3), one, one)
+        to = to + len(chunk) * 2.0 ** -38 * 448 * vs.max()
+        assert np.all(np.abs(o).max(-1) > 50 * to.max(-1))
+        assert np.all(np.abs(R.f64(out[b]) - o) <= to) and np.all(np.abs(R.f64(lse[b]) - l) <= tl)
+        at, off = at + len(pos), off + n_b[b]
+    assert lsa.lsa_get_device_status(ws) == lsa.LSA_OK
+
+
+@pytest.mark.parametrize("T,H,Hkv,rot,inter", [(1, 128, 128, 128, False), (5, 64, 64, 64, True), (2500, 32, 32, 128, False),
+                                               (14211, 2, 2, 128, True)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_rope_is_off_by_half_a_step_and_fp32s_own_errors(lsa, T, H, Hkv, rot, inter, dtype):
+    """Before the rounding to the row's type, fp32: the sum of squares (16 terms a lane, 3 joins: 20 u), its root, two
+    products, and sine and cosine within 2 u: 40 u of the pair's size, u = 2^-24. The rounding adds half a step of the
+    value, eps / 2 relative."""
+    qkv, pos, inv, w = prep_inputs(T, H, Hkv, dtype, rot, True, 1 << 20, T + H)
+    d = lsa.Dims(1, 1, 128, H, 64, N=1, k=1, kv_dtype=dtype)
+    q, k = qkv[:, :H], qkv[:, H:H + Hkv]
+    qo, ko = torch.empty_like(q.contiguous()), torch.empty_like(k.contiguous())
+    lsa.lsa_qk_norm_rope(d, lsa.QkPrep(rot, inv, *w, eps=1e-6, interleaved=inter), pos, q, k, qo, ko)
+    half = torch.finfo(q.dtype).eps / 2
+    pick = np.random.default_rng(1).permutation(T)[:400]
+    for got, x, wt in ((qo, q, w[0]), (ko, k, w[1])):
+        args = R.f64(x)[pick], pos.cpu().numpy()[pick]
+        y = R.norm_rope(*args, inv.cpu().numpy(), R.f64(wt), rot, inter, 1e-6)
+        n = np.abs(R.norm_rope(*args, np.zeros(rot // 2), R.f64(wt), rot, inter, 1e-6))
+        size = n.copy()
+        for i in range(rot // 2):
+            a, b = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+            size[..., a] = size[..., b] = np.hypot(n[..., a], n[..., b])
+        tol = size * 40 * 2.0 ** -24
+        tol = tol + (np.abs(y) + tol) * half
+        assert np.all(np.abs(R.f64(got)[pick] - y) <= tol), np.max(np.abs(R.f64(got)[pick] - y) / tol)
