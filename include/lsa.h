@@ -30,6 +30,8 @@
  *     range, a bounded wait that gave up) set bits of a sticky error word at the
  *     start of the workspace; the kernels then skip the bad item instead of
  *     faulting. lsa_get_device_status reads and clears that word.
+ *   - Values of q, K and V that are not finite are no error: the outputs that they reach
+ *     are NaN. (out = 0 with lse = -inf says that there was no token to attend to.)
  *   - Per-device facts (SM count, kernel attributes) are looked up on the first
  *     call made on a device and cached for the life of the process; the library
  *     is not meant to be used across a cudaDeviceReset.

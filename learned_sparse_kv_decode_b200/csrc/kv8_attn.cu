@@ -39,9 +39,9 @@
 //    are written at once.
 //
 // Measured (B200, bf16 queries, calls captured in a graph): 256 of 2048 chunks x 8 sequences, 16 heads, 538 MB:
-// 81 us, 6.6 TB/s (a plain copy moves 6.47); 819 of 8192 x 4, 32 heads on 8, 430 MB: 70 us, 6.1 TB/s. What is
+// 82 us, 6.5 TB/s (a plain copy moves 6.47); 819 of 8192 x 4, 32 heads on 8, 430 MB: 70 us, 6.1 TB/s. What is
 // left above the bytes is 8 to 10 us a call to start, fill and join. 32 ragged sequences with groups of 8, 355 MB:
-// 67 us, 5.3 TB/s. 8 chunks of one sequence: 6.7 us.
+// 66 us, 5.4 TB/s. 8 chunks of one sequence: 6.3 us.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -752,9 +752,9 @@ static int kv8_part_tiles(const int* tiles, int B, int64_t runs_b, int64_t slots
 // Microseconds that the runs take in parts of `per` tiles, `slots` CTAs at a time: the larger of what the
 // fullest SM computes (0.2 a tile while its 16 warps have one each, 0.137 from then on; 3.3 for a round of
 // CTAs to start and to join its warps) and what memory reads (8 KB a tile at 7 TB/s), and, where runs are left
-// to be joined, 2 for that and 0.8 for the host to launch it. Measured: 8 runs of 8 tiles 4.9 us as 8 CTAs of
-// 16 warps; of 16 tiles 6.6 so; of 32 tiles 6.2 as 64 CTAs of 4 warps; 128 runs of 16 tiles 7.3 as 128 wide
-// CTAs, 8.3 as 256 of 4 warps.
+// to be joined, 2 for that and 0.8 for the host to launch it. Measured (bf16): 8 runs of 8 tiles 4.6 us as 8
+// CTAs of 8 warps, 5.3 as 16 of 4; of 16 tiles 6.0 as 8 of 16 warps, 5.8 as 32 of 4; of 32 tiles 6.0 as 64 of 4;
+// 128 runs of 16 tiles 6.8 as 128 of 16 warps, 9.0 as 512 of 4.
 static double kv8_estimate(const int* tiles, int B, int64_t runs_b, int per, int64_t all, int num_sms, int64_t slots) {
     int64_t ctas = 0;
     for (int b = 0; b < B; ++b) ctas += runs_b * ((tiles[b] + per - 1) / per);

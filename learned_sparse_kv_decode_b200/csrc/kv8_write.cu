@@ -19,7 +19,7 @@ namespace lsa {
 //   (MANY) with four heads or fewer and tokens enough, a warp per four tokens, eight lanes to a token, each with
 //   its own eight angles: a quarter of the coefficients' work.
 // In both the next rows are loaded while the ones before are worked on. 16384 tokens of 32 + 8 heads, 336 MB,
-// take 60 us in the first form (5.6 TB/s) and 78 to 84 in the second (four rows far apart at a time), 27011 of
+// take 61 us in the first form (5.5 TB/s) and 78 to 84 in the second (four rows far apart at a time), 27011 of
 // 2 + 1 heads 25 and 14.
 constexpr int kPrepThreads = 128;
 
