@@ -93,10 +93,10 @@ __device__ __forceinline__ float kv8_ex2(float x) {
     return y;
 }
 
-// log2 of the power of two that brings 2^d, or a little less, to 2^14: an integer that fits the low bits
-// of the sum, rounded down (a whole one may be 1 less).
+// The exponent of the power of two that brings 2^d to 2^13..2^14, as an integer in the low bits of a float: adding
+// 1.5 2^23 rounds 13.5 - d to it.
 __device__ __forceinline__ float kv8_up(float d) { return (kKv8Top - 0.5f - d) + 12582912.f; }
-// That power of two (sign 1) or its inverse (-1).
+// That power of two (sign 1), or its inverse (-1): the shift leaves the exponent's bits alone.
 __device__ __forceinline__ float kv8_pow2(float up, int sign) {
     return __uint_as_float((127u << 23) + (uint32_t)sign * (__float_as_uint(up) << 23));
 }
