@@ -165,7 +165,17 @@ def _ws(ws, device):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-class Kv8Cache:
+class _Fixed:
+    """Attributes are set once. The struct that a call takes holds addresses and sizes, which another value would leave as
+    they are, while the memory behind them could go."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be changed: make a new {type(self).__name__}")
+        super().__setattr__(name, value)
+
+
+class Kv8Cache(_Fixed):
     """lsa_kv8_cache and the tensors it points to (kept alive with it).
 
     K8, V8: [sum N_b][n_kv_heads][chunk_len][Dh] float8_e4m3fn (or the same bytes as uint8);
@@ -211,7 +221,7 @@ def alloc_kv8_cache(dims, n_kv_heads, scale_block=64, device=None):
     return Kv8Cache(dims, n_kv_heads, scale_block, k8, v8, ks, vs)
 
 
-class QkPrep:
+class QkPrep(_Fixed):
     """lsa_qk_prep and the tensors it points to (kept alive with it): inv_freq [rot_dim/2], q_weight and
     k_weight [Dh] float32; a weight of None leaves those rows without a norm."""
 

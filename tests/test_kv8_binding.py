@@ -1,4 +1,4 @@
-"""CPU checks of what the 8-bit cache's binding reads from a Dims."""
+"""CPU checks of what the 8-bit cache's binding reads from a Dims, and of what its handles let a caller change."""
 import ctypes
 import types
 
@@ -64,3 +64,21 @@ def test_a_call_on_changed_dims_is_refused(monkeypatch):
     with pytest.raises(ValueError, match="12 elements, got 9"):
         lsa.lsa_kv8_decode_attn(d, cache, q, ids, None, None, out, None, ws)
     assert len(made) == 1
+
+
+def test_handles_refuse_another_value(monkeypatch):
+    """A tensor that replaced a handle's own would leave the struct with the address of freed memory."""
+    prep = lsa.QkPrep(0, eps=1e-5)
+    with pytest.raises(AttributeError, match="make a new QkPrep"):
+        prep.c = kv8._Prep()
+    with pytest.raises(AttributeError, match="make a new QkPrep"):
+        prep.tensors = (None, None, None)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)  # stands for tensors on a GPU
+    codes = torch.zeros(20, 4, 64, 128, dtype=torch.uint8)
+    scales = torch.zeros(20, 4, 1)
+    cache = lsa.Kv8Cache(ragged(), 4, 64, codes, codes.clone(), scales, scales.clone())
+    for name in ("K8", "V8", "k_scale", "v_scale", "n_kv_heads", "scale_block", "chunks", "C", "c", "ptr"):
+        with pytest.raises(AttributeError, match="make a new Kv8Cache"):
+            setattr(cache, name, getattr(cache, name))
+    assert cache.K8 is codes and cache.c.K8 == codes.data_ptr()
+    cache.K8[0] = 1  # what they hold may change
