@@ -45,7 +45,7 @@ typedef struct {
  *   a_i = position * inv_freq[i], i < rot_dim/2     (the product and its reduction in 64 bits)
  *   (y_p, y_r) <- (y_p cos a_i - y_r sin a_i, y_r cos a_i + y_p sin a_i)
  * with the pair (p, r) = (i, i + rot_dim/2), or (2i, 2i + 1) if `interleaved`. Values from rot_dim on
- * are not rotated. Computed in fp32 and rounded once to kv_dtype. */
+ * are not rotated. Computed in fp32, the mean of squares too (values below 2^60), and rounded once to kv_dtype. */
 typedef struct {
     int32_t rot_dim;         /* a multiple of 16, 0..Dh */
     int32_t interleaved;     /* 0 or 1 */
